@@ -96,6 +96,18 @@ _SIGS = {
     "orthrus_commit_adaptive": [_P, C.POINTER(KV), _I, _I, _P, _P, _P, _P, _P, _P],
     "orthrus_check_error": [_P, _P, C.POINTER(C.c_uint32)],
     "orthrus_set_probe": [_P, _I, _I, _I, C.POINTER(_P), C.POINTER(_P), _I],
+    "orthrus_embed_rows": [_P, _I, _I, _I, _P, _I, C.c_float, _P, _I, _P, _P],
+    "orthrus_embed_grad_workspace": [_I, _I, _I, C.POINTER(C.c_size_t)],
+    "orthrus_embed_grad": [_P, _I, _P, _I, _I, _I, C.c_float, _I, _P, _I, _P, C.c_size_t, _P, _P],
+    "orthrus_rmsnorm": [_P, _I, _P, _I, _I, _I, C.c_float, _P, _P],
+    "orthrus_rmsnorm_grad_workspace": [_I, _I, C.POINTER(C.c_size_t)],
+    "orthrus_rmsnorm_grad": [_P, _I, _P, _P, _I, _I, _I, C.c_float, _P, _P, _P, C.c_size_t, _P],
+    "orthrus_ce_lm_head_workspace": [_I, _I, _I, _I, C.POINTER(C.c_size_t)],
+    "orthrus_ce_lm_head": [_P, _P, _I, _P, _I, _I, _I, _P, _P, _P, C.c_size_t, _P, _P],
+    "orthrus_ce_lm_head_grad_workspace": [_I, _I, _I, _I, _I, C.POINTER(C.c_size_t)],
+    "orthrus_ce_lm_head_grad": [_P, _P, _I, _P, _P, _P, _I, _I, _I, _P, _P, _P, C.c_size_t, _P, _P],
+    "orthrus_kl_lm_head_grad_workspace": [_I, _I, _I, _I, C.POINTER(C.c_size_t)],
+    "orthrus_kl_lm_head_grad": [_P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _P, _P, C.c_size_t, _P, _P],
     "orthrus_dual_view_attention_noalloc": [C.POINTER(Config), C.POINTER(KV), _I, _I, _P, _P, _P, _I, _I, _P, _P,
                                             _P],
 }
@@ -161,6 +173,220 @@ def _need(x, dtype, name):
     """Marshalling check: a contiguous device tensor of the dtype the C call reads."""
     if x.dtype != dtype or not x.is_cuda or not x.is_contiguous():
         raise TypeError(f"{name}: expected a contiguous CUDA {dtype} tensor, got {x.dtype} on {x.device}")
+
+
+# -------------------------------------------- training-side operators
+# Context-free mirrors: outputs and workspaces come from torch's allocator on
+# the tensors' device and that device's current stream.  `err` is an optional
+# int32 device tensor of one element that collects the ORTHRUS_DEVERR_* bits.
+_DT = None      # torch dtype -> orthrus_dtype_t
+
+
+def _dtype_id(name, t):
+    global _DT
+    if _DT is None:
+        import torch
+        _DT = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+    d = _DT.get(t)
+    if d is None:
+        raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, got {t}")
+    return d
+
+
+def _need_rows(name, x, dtypes, shape, device=None):
+    """A contiguous CUDA tensor of one of `dtypes` and of `shape` (None: any
+    extent), on `device` when given."""
+    if not x.is_cuda or not x.is_contiguous() or x.dtype not in dtypes:
+        raise TypeError(f"{name}: expected a contiguous CUDA tensor of {' or '.join(str(d) for d in dtypes)}, got "
+                        f"{x.dtype} on {x.device}{'' if x.is_contiguous() else ', not contiguous'}")
+    if device is not None and x.device != device:
+        raise ValueError(f"{name}: on {x.device}, the other arguments on {device}")
+    if x.dim() != len(shape) or any(s is not None and int(n) != s for n, s in zip(x.shape, shape)):
+        raise ValueError(f"{name}: expected shape {tuple('*' if s is None else s for s in shape)}, got "
+                         f"{tuple(int(n) for n in x.shape)}")
+    return x
+
+
+class _OnDevice:
+    """The call's device made current for the launches, and its stream."""
+
+    def __init__(self, device):
+        import torch
+        self.torch = torch
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return C.c_void_p(self.torch.cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _train_ws(name, device, *args):
+    """Workspace of one call: (tensor, 256-byte aligned pointer, bytes)."""
+    import torch
+    n = C.c_size_t()
+    _check(name, getattr(lib(), name)(*args, C.byref(n)))
+    if n.value == 0:
+        return None, None, 0
+    ws = torch.empty(n.value + 256, dtype=torch.uint8, device=device)
+    return ws, C.c_void_p((ws.data_ptr() + 255) & ~255), n.value
+
+
+def _err_ptr(err, device):
+    import torch
+    if err is None:
+        return None
+    _need_rows("err", err, (torch.int32,), (1,), device)
+    return _ptr(err)
+
+
+def orthrus_embed_rows(table, ids, scale=1.0, out_dtype=None, err=None):
+    """scale * table[ids]: table [vocab, hidden] (bf16 or fp32), ids int32
+    [rows] (negative: a zero row).  Returns [rows, hidden] of out_dtype (default
+    fp32, the residual stream's)."""
+    import torch
+    _need_rows("table", table, (torch.bfloat16, torch.float32), (None, None))
+    dev = table.device
+    _need_rows("ids", ids, (torch.int32,), (None,), dev)
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    od = _dtype_id("out_dtype", out_dtype)
+    V, d = table.shape
+    n = ids.shape[0]
+    with _OnDevice(dev) as stream:
+        out = torch.empty((n, d), dtype=out_dtype, device=dev)
+        _check("orthrus_embed_rows", lib().orthrus_embed_rows(
+            _ptr(table), _dtype_id("table", table.dtype), V, d, _ptr(ids), n, float(scale), _ptr(out), od,
+            _err_ptr(err, dev), stream))
+    return out
+
+
+def orthrus_embed_grad(dout, ids, vocab, scale=1.0, dtype=None, out=None, accumulate=False, err=None):
+    """Gradient of orthrus_embed_rows in its table: [vocab, hidden] of `dtype`
+    (default dout's), zeros for ids that do not occur.  With `out` the result is
+    written there, or added to it when accumulate is set."""
+    import torch
+    fl = (torch.bfloat16, torch.float32)
+    _need_rows("dout", dout, fl, (None, None))
+    dev = dout.device
+    n, d = dout.shape
+    _need_rows("ids", ids, (torch.int32,), (n,), dev)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out is not None:
+        _need_rows("out", out, fl if dtype is None else (dtype,), (int(vocab), d), dev)
+    with _OnDevice(dev) as stream:
+        if out is None:
+            out = torch.empty((int(vocab), d), dtype=dout.dtype if dtype is None else dtype, device=dev)
+        od = _dtype_id("dtype", out.dtype)
+        ws, wp, wn = _train_ws("orthrus_embed_grad_workspace", dev, n, d, int(vocab))
+        _check("orthrus_embed_grad", lib().orthrus_embed_grad(
+            _ptr(dout), _dtype_id("dout", dout.dtype), _ptr(ids), n, d, int(vocab), float(scale), int(bool(accumulate)),
+            _ptr(out), od, wp, wn, _err_ptr(err, dev), stream))
+    return out
+
+
+def orthrus_rmsnorm(x, gain, eps):
+    """x * gain / sqrt(mean(x^2) + eps) per row: x [rows, hidden] fp32 or gain's
+    dtype; the result has gain's dtype."""
+    import torch
+    fl = (torch.bfloat16, torch.float32)
+    _need_rows("x", x, fl, (None, None))
+    n, d = x.shape
+    _need_rows("gain", gain, fl, (d,), x.device)
+    with _OnDevice(x.device) as stream:
+        y = torch.empty((n, d), dtype=gain.dtype, device=x.device)
+        _check("orthrus_rmsnorm", lib().orthrus_rmsnorm(
+            _ptr(x), _dtype_id("x", x.dtype), _ptr(gain), _dtype_id("gain", gain.dtype), n, d, float(eps), _ptr(y),
+            stream))
+    return y
+
+
+def orthrus_rmsnorm_grad(x, gain, dy, eps):
+    """Gradient of orthrus_rmsnorm: (dx [rows, hidden] of x's dtype, dgain fp32
+    [hidden])."""
+    import torch
+    fl = (torch.bfloat16, torch.float32)
+    _need_rows("x", x, fl, (None, None))
+    dev = x.device
+    n, d = x.shape
+    _need_rows("gain", gain, fl, (d,), dev)
+    _need_rows("dy", dy, (gain.dtype,), (n, d), dev)
+    with _OnDevice(dev) as stream:
+        dx = torch.empty_like(x)
+        dgain = torch.empty(d, dtype=torch.float32, device=dev)
+        ws, wp, wn = _train_ws("orthrus_rmsnorm_grad_workspace", dev, n, d)
+        _check("orthrus_rmsnorm_grad", lib().orthrus_rmsnorm_grad(
+            _ptr(x), _dtype_id("x", x.dtype), _ptr(gain), _ptr(dy), _dtype_id("gain", gain.dtype), n, d, float(eps),
+            _ptr(dx), _ptr(dgain), wp, wn, stream))
+    return dx, dgain
+
+
+def orthrus_ce_lm_head(h, w, targets, err=None):
+    """Cross entropy through the LM head w [vocab, hidden] of the hidden rows h
+    [rows, hidden] (same dtype): (loss, lse), fp32 [rows].  targets int32
+    [rows]; negative: an ignored row (loss 0)."""
+    import torch
+    _need_rows("h", h, (torch.bfloat16, torch.float32), (None, None))
+    dev = h.device
+    n, d = h.shape
+    _need_rows("w", w, (h.dtype,), (None, d), dev)
+    _need_rows("targets", targets, (torch.int32,), (n,), dev)
+    V, dt = w.shape[0], _dtype_id("h", h.dtype)
+    with _OnDevice(dev) as stream:
+        loss = torch.empty(n, dtype=torch.float32, device=dev)
+        lse = torch.empty_like(loss)
+        ws, wp, wn = _train_ws("orthrus_ce_lm_head_workspace", dev, n, d, V, dt)
+        _check("orthrus_ce_lm_head", lib().orthrus_ce_lm_head(
+            _ptr(h), _ptr(w), dt, _ptr(targets), n, d, V, _ptr(loss), _ptr(lse), wp, wn, _err_ptr(err, dev), stream))
+    return loss, lse
+
+
+def orthrus_ce_lm_head_grad(h, w, targets, lse, dloss, weight_grad=True, err=None):
+    """Gradient of orthrus_ce_lm_head from its lse and the upstream dloss (fp32
+    [rows]): (dh [rows, hidden], dw [vocab, hidden] or None), h's dtype."""
+    import torch
+    _need_rows("h", h, (torch.bfloat16, torch.float32), (None, None))
+    dev = h.device
+    n, d = h.shape
+    _need_rows("w", w, (h.dtype,), (None, d), dev)
+    _need_rows("targets", targets, (torch.int32,), (n,), dev)
+    _need_rows("lse", lse, (torch.float32,), (n,), dev)
+    _need_rows("dloss", dloss, (torch.float32,), (n,), dev)
+    V, dt = w.shape[0], _dtype_id("h", h.dtype)
+    with _OnDevice(dev) as stream:
+        dh = torch.empty_like(h)
+        dw = torch.empty_like(w) if weight_grad else None
+        ws, wp, wn = _train_ws("orthrus_ce_lm_head_grad_workspace", dev, n, d, V, dt, int(bool(weight_grad)))
+        _check("orthrus_ce_lm_head_grad", lib().orthrus_ce_lm_head_grad(
+            _ptr(h), _ptr(w), dt, _ptr(targets), _ptr(lse), _ptr(dloss), n, d, V, _ptr(dh), _ptr(dw), wp, wn,
+            _err_ptr(err, dev), stream))
+    return dh, dw
+
+
+def orthrus_kl_lm_head_grad(h_ar, h_diff, w, lse_ar, lse_diff, dkl, err=None):
+    """Gradient of the forward KL(softmax(w h_ar) || softmax(w h_diff)) in
+    h_diff, from both log-sum-exps and the upstream dkl (fp32 [rows]): dh_diff
+    [rows, hidden], h_diff's dtype."""
+    import torch
+    _need_rows("h_ar", h_ar, (torch.bfloat16, torch.float32), (None, None))
+    dev = h_ar.device
+    n, d = h_ar.shape
+    _need_rows("h_diff", h_diff, (h_ar.dtype,), (n, d), dev)
+    _need_rows("w", w, (h_ar.dtype,), (None, d), dev)
+    for name, x in (("lse_ar", lse_ar), ("lse_diff", lse_diff), ("dkl", dkl)):
+        _need_rows(name, x, (torch.float32,), (n,), dev)
+    V, dt = w.shape[0], _dtype_id("h_ar", h_ar.dtype)
+    with _OnDevice(dev) as stream:
+        dh = torch.empty_like(h_diff)
+        ws, wp, wn = _train_ws("orthrus_kl_lm_head_grad_workspace", dev, n, d, V, dt)
+        _check("orthrus_kl_lm_head_grad", lib().orthrus_kl_lm_head_grad(
+            _ptr(h_ar), _ptr(h_diff), _ptr(w), dt, _ptr(lse_ar), _ptr(lse_diff), _ptr(dkl), n, d, V, _ptr(dh), wp, wn,
+            _err_ptr(err, dev), stream))
+    return dh
 
 
 class Engine:
@@ -231,6 +457,7 @@ class Engine:
                                                       C.c_size_t(self.ws_bytes), C.byref(ctx)))
         self.ctx = ctx
         self.step = torch.zeros(1, dtype=torch.int64, device=self.device)
+        self.train_err = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def __del__(self):
         try:
@@ -385,6 +612,48 @@ class Engine:
         _check("orthrus_kl_lm_head", lib().orthrus_kl_lm_head(
             self.ctx, _ptr(h_ar), _ptr(h_diff), rows, _ptr(kl), _ptr(la), _ptr(ld), _stream()))
         return kl, la, ld
+
+    # training-side operators over the engine's own weights (their device
+    # checks collect in train_err)
+    def embed_rows(self, ids, scale=1.0):
+        """scale * embed[ids]: the fp32 residual rows of int32 ids [rows]."""
+        return orthrus_embed_rows(self.embed, self._i32(ids), scale, err=self.train_err)
+
+    def embed_grad(self, dout, ids, scale=1.0, out=None, accumulate=False):
+        """Gradient of embed_rows in the embedding table."""
+        return orthrus_embed_grad(dout, self._i32(ids), self.shape.vocab, scale, out=out, accumulate=accumulate,
+                                  err=self.train_err)
+
+    def final_norm_rows(self, x):
+        """The norm in front of the LM head: fp32 (or model-dtype) rows to the
+        model dtype."""
+        return orthrus_rmsnorm(x, self.final_norm, self.shape.rms_eps)
+
+    def final_norm_grad(self, x, dy):
+        """(dx, dgain) of final_norm_rows."""
+        return orthrus_rmsnorm_grad(x, self.final_norm, dy, self.shape.rms_eps)
+
+    def ce_lm_head(self, h, targets):
+        """Cross entropy of final-normed rows h through the LM head: (loss,
+        lse), fp32 [rows]."""
+        return orthrus_ce_lm_head(h, self.lm_head, self._i32(targets), err=self.train_err)
+
+    def ce_lm_head_grad(self, h, targets, lse, dloss, weight_grad=True):
+        """(dh, dw) of ce_lm_head; weight_grad False leaves dw out (a frozen
+        head)."""
+        return orthrus_ce_lm_head_grad(h, self.lm_head, self._i32(targets), lse, dloss, weight_grad,
+                                       err=self.train_err)
+
+    def kl_lm_head_grad(self, h_ar, h_diff, lse_ar, lse_diff, dkl):
+        """Gradient of kl_lm_head in h_diff, from its log-sum-exps."""
+        return orthrus_kl_lm_head_grad(h_ar, h_diff, self.lm_head, lse_ar, lse_diff, dkl, err=self.train_err)
+
+    def check_train_error(self):
+        """The device check bits of this engine's training-side calls so far
+        (0: none), read and cleared."""
+        bits = int(self.train_err.item())
+        self.train_err.zero_()
+        return bits
 
     def tree_topw(self, logits, width):
         """The `width` best ids and logits of each fp32 logits row, and the

@@ -1,0 +1,91 @@
+// Internal declarations of the training-side row and vocabulary-loss
+// kernels (orthrus_embed_rows .. orthrus_kl_lm_head_grad): they need no
+// context, so their scratch is a plan over the caller's workspace.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/orthrus.h"
+
+namespace orthrus {
+
+// Offsets into a caller's workspace, each 256-byte aligned.
+struct WsPlan {
+    size_t total = 0;
+    size_t take(size_t bytes)
+    {
+        const size_t o = total;
+        total += (bytes + 255) & ~(size_t)255;
+        return o;
+    }
+};
+
+// ------------------------------------------------------------- embedding
+struct EmbedRowsArgs {
+    const void *table;
+    const int32_t *ids;
+    void *out;
+    int dtype, out_dtype, rows, d, vocab;
+    float scale;
+    unsigned *err;
+};
+cudaError_t launch_embed_rows(const EmbedRowsArgs &a, cudaStream_t s);
+
+constexpr int kSortSmall = 8192;   // most rows sorted by one block
+constexpr int kSortTile = 2048;    // keys per block of the radix sort
+constexpr int kSortDigit = 9;      // widest radix digit
+
+struct EmbedGradPlan {
+    size_t total, o_tok[2], o_idx[2], o_hist, o_part;
+    int piece;     // sorted rows per piece
+    int pieces;
+    int digits, digit_bits, tiles;   // radix sort (rows > kSortSmall)
+};
+EmbedGradPlan plan_embed_grad(int rows, int vocab, int d);
+struct EmbedGradArgs {
+    const void *dout;
+    const int32_t *ids;
+    void *dtable;
+    int dout_dtype, dtable_dtype, rows, d, vocab, accumulate;
+    float scale;
+    char *ws;
+    unsigned *err;
+};
+cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t s);
+
+// --------------------------------------------------------------- RMSNorm
+struct NormArgs {
+    const void *x, *gain, *dy;
+    void *out;        // y, or dx
+    float *dgain;
+    int x_dtype, dtype, rows, d;
+    float eps;
+    char *ws;
+};
+cudaError_t launch_norm_rows(const NormArgs &a, cudaStream_t s);
+size_t norm_grad_workspace(int rows, int d);
+cudaError_t launch_norm_grad(const NormArgs &a, cudaStream_t s);
+
+// -------------------------------------------------------- vocabulary loss
+// One loss call: z = h W^T over V ids.  KL: h holds the AR rows, h2 the
+// diffusion rows, and lse / lse2 their log-sum-exps.
+struct LossArgs {
+    const void *h, *h2, *w;
+    const int32_t *targets;   // CE: [N], negative = ignored row
+    const float *lse_in, *lse2_in, *g;
+    float *loss, *lse;        // CE forward outputs
+    void *dh, *dw;            // gradients (dw nullable)
+    int dtype, N, d, V;
+    int kl;
+    char *ws;
+    unsigned *err;
+};
+
+size_t loss_fwd_workspace(int N, int d, int V, int dtype);
+size_t loss_grad_workspace(int N, int d, int V, int dtype, int want_dw, int kl);
+cudaError_t launch_loss_fwd(const LossArgs &a, cudaStream_t s);
+cudaError_t launch_loss_grad(const LossArgs &a, cudaStream_t s);
+
+}  // namespace orthrus

@@ -1,0 +1,853 @@
+// Row operators of the training side: the token embedding with scaling and
+// its gradient by sorted tokens, and RMSNorm with its gradient.  All of them
+// are bound by memory traffic (large calls) or launch latency (small ones).
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "train.h"
+
+namespace orthrus {
+
+// ---------------------------------------------------------------- vectors
+// VEC elements of T as fp32: 16-byte accesses when VEC = 8 (two for fp32),
+// else one element at a time (odd row lengths, unaligned buffers).
+template <class T, int VEC> struct RowVec;
+template <class T> struct RowVec<T, 1> {
+    static __device__ __forceinline__ void load(const T *p, float (&v)[1]) { v[0] = to_f<T>(*p); }
+    static __device__ __forceinline__ void store(T *p, const float (&v)[1]) { *p = from_f<T>(v[0]); }
+};
+template <> struct RowVec<float, 8> {
+    static __device__ __forceinline__ void load(const float *p, float (&v)[8])
+    {
+        const float4 a = ((const float4 *)p)[0], b = ((const float4 *)p)[1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float (&v)[8])
+    {
+        ((float4 *)p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        ((float4 *)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+template <> struct RowVec<bf16, 8> {
+    static __device__ __forceinline__ void load(const bf16 *p, float (&v)[8])
+    {
+        const uint4 u = *(const uint4 *)p;
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {   // bf16 -> fp32 is a shift
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(bf16 *p, const float (&v)[8])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *(const uint32_t *)&h;
+        }
+        *(uint4 *)p = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+static bool rows_aligned(const void *p, int d) { return ((uintptr_t)p & 15) == 0 && d % 8 == 0; }
+
+// ---------------------------------------------------------------- embedding
+// out[r] = scale * table[ids[r]]; a negative id is padding (a zero row).
+constexpr int kEmbThreads = 256;
+
+template <class T, class TO, int VEC>
+__global__ void __launch_bounds__(kEmbThreads) embed_rows_kernel(const T *table, const int32_t *ids, TO *out, int d,
+                                                                 int vocab, float scale, unsigned *err)
+{
+    constexpr int Q = 16 / VEC > 4 ? 4 : 16 / VEC;   // chunks of a thread in flight
+    pdl_trigger();
+    pdl_wait();
+    const int row = blockIdx.x;
+    const int id = ids[row];
+    const bool ok = id >= 0 && id < vocab;
+    if (id >= vocab && threadIdx.x == 0 && blockIdx.y == 0 && err) raise_err(err, ORTHRUS_DEVERR_TOKEN);
+    const T *src = table + (size_t)(ok ? id : 0) * d;
+    TO *dst = out + (size_t)row * d;
+    const int nc = d / VEC, step = gridDim.y * Q * kEmbThreads;
+    for (int c0 = blockIdx.y * Q * kEmbThreads + threadIdx.x; c0 < nc; c0 += step) {
+        float v[Q][VEC];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int c = c0 + q * kEmbThreads;
+            if (ok && c < nc) RowVec<T, VEC>::load(src + (size_t)c * VEC, v[q]);
+            else
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[q][i] = 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int c = c0 + q * kEmbThreads;
+            if (c >= nc) continue;
+            // (0 * scale stays 0 for a padding row unless the scale is not finite)
+            if (ok)
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[q][i] *= scale;
+            RowVec<TO, VEC>::store(dst + (size_t)c * VEC, v[q]);
+        }
+    }
+}
+
+template <class T, class TO> static cudaError_t embed_rows_t(const EmbedRowsArgs &a, cudaStream_t s)
+{
+    const bool vec = rows_aligned(a.table, a.d) && rows_aligned(a.out, a.d);
+    const int per = vec ? 8 * 2 * kEmbThreads : 4 * kEmbThreads;   // elements a block covers per step
+    // one block per row and slab of the row, so that every element is in
+    // flight at once; rows beyond 64 slabs loop
+    const dim3 grid(a.rows, std::min(64, (a.d + per - 1) / per));
+    if (vec)
+        return launch_k(embed_rows_kernel<T, TO, 8>, grid, kEmbThreads, 0, s, (const T *)a.table, a.ids, (TO *)a.out,
+                        a.d, a.vocab, a.scale, a.err);
+    return launch_k(embed_rows_kernel<T, TO, 1>, grid, kEmbThreads, 0, s, (const T *)a.table, a.ids, (TO *)a.out, a.d,
+                    a.vocab, a.scale, a.err);
+}
+
+cudaError_t launch_embed_rows(const EmbedRowsArgs &a, cudaStream_t s)
+{
+    const bool ib = a.dtype == ORTHRUS_BF16, ob = a.out_dtype == ORTHRUS_BF16;
+    if (ib) return ob ? embed_rows_t<bf16, bf16>(a, s) : embed_rows_t<bf16, float>(a, s);
+    return ob ? embed_rows_t<float, bf16>(a, s) : embed_rows_t<float, float>(a, s);
+}
+
+// ------------------------------------------------------- embedding gradient
+// dE[v] = scale * sum over the rows r with ids[r] = v of dout[r], summed in
+// fp32 in row order: the rows are sorted by token (stable), the sorted list
+// is cut into pieces of equal length, a piece sums its runs of equal tokens,
+// and a run that crosses pieces leaves one partial sum in each, joined in
+// order afterwards.  A draft block's 31 mask tokens make one token 97 % of
+// the rows, so a run has to be shared by many blocks; the fixed cut and
+// order give the same bits on every call (no floating-point atomics).
+// Ids outside [0, vocab) sort behind every token and are left out.
+EmbedGradPlan plan_embed_grad(int rows, int vocab, int d)
+{
+    EmbedGradPlan p{};
+    WsPlan w;
+    for (int i = 0; i < 2; ++i) {
+        p.o_tok[i] = w.take((size_t)rows * 4);
+        p.o_idx[i] = w.take((size_t)rows * 4);
+    }
+    int bits = 1;
+    while (bits < 31 && (vocab >> bits) != 0) ++bits;   // keys 0 .. vocab
+    p.digits = (bits + kSortDigit - 1) / kSortDigit;
+    p.digit_bits = (bits + p.digits - 1) / p.digits;
+    p.tiles = (rows + kSortTile - 1) / kSortTile;
+    p.o_hist = w.take(rows > kSortSmall ? ((size_t)p.tiles << p.digit_bits) * 4 : 0);
+    // pieces: short enough that the rows spread over the SMs, long enough
+    // that at most ~1024 partials per column wait to be joined
+    p.piece = 32;
+    while (p.piece < 4096 && rows / p.piece > 1024) p.piece *= 2;
+    p.pieces = (rows + p.piece - 1) / p.piece;
+    p.o_part = w.take((size_t)p.pieces * 2 * d * 4);
+    p.total = w.total;
+    return p;
+}
+
+__device__ __forceinline__ int sort_key(const int32_t *ids, int r, int vocab, unsigned *err)
+{
+    const int id = ids[r];
+    if (id >= vocab && err) raise_err(err, ORTHRUS_DEVERR_TOKEN);
+    return id < 0 || id >= vocab ? vocab : id;
+}
+
+// Zeros of the whole gradient (the rows of tokens that do not occur), by
+// blocks first .. of the launch.
+__device__ __forceinline__ void fill_zero(void *p, size_t bytes, int first)
+{
+    const size_t n16 = (((uintptr_t)p & 15) == 0) ? bytes / 16 : 0;
+    const size_t t = (size_t)(blockIdx.x - first) * blockDim.x + threadIdx.x;
+    const size_t n = (size_t)(gridDim.x - first) * blockDim.x;
+    for (size_t i = t; i < n16; i += n) ((uint4 *)p)[i] = make_uint4(0, 0, 0, 0);
+    for (size_t i = n16 * 16 + t * 2; i + 1 < bytes; i += n * 2) *(uint16_t *)((char *)p + i) = 0;
+}
+
+constexpr int kSortThreads = 1024;
+
+// Up to kSortSmall rows: block 0 sorts (token, row) pairs in shared memory
+// (bitonic network: comparisons fixed by the size alone), the other blocks
+// write the zeros meanwhile.
+template <class K>
+__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const int32_t *ids, int rows, int vocab, int row_bits,
+                                                                  int32_t *tok, int32_t *idx, void *zero,
+                                                                  size_t zero_bytes, unsigned *err)
+{
+    extern __shared__ __align__(16) unsigned char sort_smem[];
+    K *key = (K *)sort_smem;
+    pdl_trigger();
+    pdl_wait();
+    if (blockIdx.x > 0) {
+        fill_zero(zero, zero_bytes, 1);
+        return;
+    }
+    int n = 2;
+    while (n < rows) n <<= 1;
+    for (int i = threadIdx.x; i < n; i += kSortThreads)
+        key[i] = i < rows ? (((K)sort_key(ids, i, vocab, err) << row_bits) | (K)i) : ~(K)0;
+    for (int k = 2; k <= n; k <<= 1)
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            __syncthreads();
+            for (int p = threadIdx.x; p < n / 2; p += kSortThreads) {
+                const int lo = 2 * p - (p & (j - 1)), hi = lo + j;   // pair p of distance j
+                const K a = key[lo], b = key[hi];
+                if ((a > b) == ((lo & k) == 0)) { key[lo] = b; key[hi] = a; }
+            }
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows; i += kSortThreads) {
+        tok[i] = (int32_t)(key[i] >> row_bits);
+        idx[i] = (int32_t)(key[i] & (((K)1 << row_bits) - 1));
+    }
+}
+
+// More rows: least-significant-digit radix sort, one launch each for a
+// digit's histograms (per tile of kSortTile keys), their exclusive scan, and
+// the stable scatter.
+constexpr int kRadixThreads = 256, kRadixWarps = kRadixThreads / 32, kRadixPer = kSortTile / kRadixThreads;
+
+template <bool FIRST>
+__global__ void __launch_bounds__(kRadixThreads) radix_hist_kernel(const int32_t *src, int rows, int vocab, int tiles,
+                                                                   int shift, int bits, int *hist, void *zero,
+                                                                   size_t zero_bytes, unsigned *err)
+{
+    __shared__ int h[1 << kSortDigit];
+    pdl_trigger();
+    pdl_wait();
+    if ((int)blockIdx.x >= tiles) {
+        fill_zero(zero, zero_bytes, tiles);
+        return;
+    }
+    for (int i = threadIdx.x; i < (1 << bits); i += kRadixThreads) h[i] = 0;
+    __syncthreads();
+    const int base = blockIdx.x * kSortTile;
+#pragma unroll
+    for (int j = 0; j < kRadixPer; ++j) {
+        const int i = base + j * kRadixThreads + threadIdx.x;
+        const int k = i < rows ? (FIRST ? sort_key(src, i, vocab, err) : src[i]) : -1;
+        const int dg = k < 0 ? -1 : (k >> shift) & ((1 << bits) - 1);
+        // one atomic per distinct digit of the warp (most rows may share one)
+        const unsigned m = __match_any_sync(0xffffffffu, dg);
+        if (dg >= 0 && (threadIdx.x & 31) == __ffs(m) - 1) atomicAdd(&h[dg], __popc(m));
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < (1 << bits); i += kRadixThreads) hist[(size_t)i * tiles + blockIdx.x] = h[i];
+}
+
+// exclusive scan of n ints in place by one block
+__global__ void __launch_bounds__(1024) radix_scan_kernel(int *h, int n)
+{
+    __shared__ int warp_tot[32];
+    pdl_trigger();
+    pdl_wait();
+    int carry = 0;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int b = 0; b < n; b += 4096) {
+        int v[4], t = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = b + threadIdx.x * 4 + j;
+            v[j] = i < n ? h[i] : 0;
+            t += v[j];
+        }
+        int x = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) warp_tot[warp] = x;
+        __syncthreads();
+        if (warp == 0) {
+            int w = warp_tot[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, w, o);
+                if (lane >= o) w += y;
+            }
+            warp_tot[lane] = w;
+        }
+        __syncthreads();
+        int e = carry + (warp ? warp_tot[warp - 1] : 0) + x - t;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = b + threadIdx.x * 4 + j;
+            if (i < n) h[i] = e;
+            e += v[j];
+        }
+        carry += warp_tot[31];
+        __syncthreads();
+    }
+}
+
+template <bool FIRST>
+__global__ void __launch_bounds__(kRadixThreads) radix_scatter_kernel(const int32_t *src_tok, const int32_t *src_idx,
+                                                                      int rows, int vocab, int tiles, int shift, int bits,
+                                                                      const int *hist, int32_t *tok, int32_t *idx)
+{
+    __shared__ int cnt[kRadixWarps][1 << kSortDigit];
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nb = 1 << bits;
+    for (int i = threadIdx.x; i < kRadixWarps * nb; i += kRadixThreads) cnt[i / nb][i % nb] = 0;
+    __syncthreads();
+    // a warp owns kRadixPer x 32 consecutive keys, 32 at a time
+    const int base = blockIdx.x * kSortTile + warp * 32 * kRadixPer;
+    int key[kRadixPer], rank[kRadixPer];
+#pragma unroll
+    for (int j = 0; j < kRadixPer; ++j) {
+        const int i = base + j * 32 + lane;
+        key[j] = i < rows ? (FIRST ? sort_key(src_tok, i, vocab, nullptr) : src_tok[i]) : -1;
+        const int dg = key[j] < 0 ? nb : (key[j] >> shift) & (nb - 1);
+        const unsigned m = __match_any_sync(0xffffffffu, dg);
+        const int before = __popc(m & ((1u << lane) - 1));
+        int at = 0;
+        if (dg < nb) at = cnt[warp][dg];
+        __syncwarp();
+        if (dg < nb && before == 0) cnt[warp][dg] = at + __popc(m);
+        __syncwarp();
+        rank[j] = at + before;
+    }
+    __syncthreads();
+    // counts -> first position of (digit, warp) in the output
+    for (int dg = threadIdx.x; dg < nb; dg += kRadixThreads) {
+        int e = hist[(size_t)dg * tiles + blockIdx.x];
+        for (int w = 0; w < kRadixWarps; ++w) {
+            const int c = cnt[w][dg];
+            cnt[w][dg] = e;
+            e += c;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kRadixPer; ++j) {
+        const int i = base + j * 32 + lane;
+        if (i >= rows) continue;
+        const int pos = cnt[warp][(key[j] >> shift) & (nb - 1)] + rank[j];
+        tok[pos] = key[j];
+        idx[pos] = FIRST ? i : src_idx[i];
+    }
+}
+
+// One block per (piece, column slab): runs of equal tokens summed in fp32.
+constexpr int kRunThreads = 128;
+
+template <class T, class TG, int VEC>
+__global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const T *dout, const int32_t *tok, const int32_t *idx,
+                                                              int rows, int d, int vocab, int P, float scale,
+                                                              int accumulate, TG *dtable, float *part)
+{
+    constexpr int J = VEC == 8 ? 1 : 4;      // column chunks of a thread
+    constexpr int U = VEC == 8 ? 8 : 4;      // rows in flight
+    extern __shared__ int run_smem[];
+    int *st = run_smem, *si = run_smem + P;
+    pdl_trigger();
+    pdl_wait();
+    const int lo = blockIdx.x * P, hi = min(rows, lo + P), n = hi - lo;
+    for (int i = threadIdx.x; i < n; i += kRunThreads) { st[i] = tok[lo + i]; si[i] = idx[lo + i]; }
+    const int prev = lo > 0 ? tok[lo - 1] : -1, next = hi < rows ? tok[hi] : -1;
+    __syncthreads();
+    const int c0 = blockIdx.y * kRunThreads * J;
+    float acc[J][VEC];
+    auto clear = [&]() {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) acc[j][e] = 0.f;
+    };
+    auto flush = [&](int token, int b, int e) {   // run [b, e) of the piece
+        if (token >= vocab) return;
+        const bool head = b == 0 && prev == token, tail = e == n && next == token;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int c = (c0 + j * kRunThreads + threadIdx.x) * VEC;
+            if (c >= d) continue;
+            if (head || tail) {
+                float *p = part + ((size_t)blockIdx.x * 2 + (head ? 0 : 1)) * d + c;
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) p[q] = acc[j][q];
+            } else {
+                TG *o = dtable + (size_t)token * d + c;
+                float old[VEC], v[VEC];
+                if (accumulate) RowVec<TG, VEC>::load(o, old);
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) v[q] = accumulate ? fmaf(scale, acc[j][q], old[q]) : scale * acc[j][q];
+                RowVec<TG, VEC>::store(o, v);
+            }
+        }
+    };
+    clear();
+    int cur = st[0], begin = 0;
+    for (int r0 = 0; r0 < n; r0 += U) {
+        float v[U][J][VEC];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int c = (c0 + j * kRunThreads + threadIdx.x) * VEC;
+                if (r0 + u < n && c < d && st[r0 + u] < vocab)
+                    RowVec<T, VEC>::load(dout + (size_t)si[r0 + u] * d + c, v[u][j]);
+                else
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) v[u][j][e] = 0.f;
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r0 + u >= n) break;
+            const int t = st[r0 + u];
+            if (t != cur) {
+                flush(cur, begin, r0 + u);
+                clear();
+                cur = t;
+                begin = r0 + u;
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) acc[j][e] += v[u][j][e];
+        }
+    }
+    flush(cur, begin, n);
+}
+
+// Runs that cross pieces: the piece a run starts in adds up its partials in
+// order.  32 columns x 8 strands of pieces per block; the strands join in
+// order too.
+constexpr int kJoinCols = 32, kJoinStrands = 8;
+
+template <class TG>
+__global__ void __launch_bounds__(kJoinCols *kJoinStrands) run_join_kernel(const int32_t *tok, int rows, int d, int vocab,
+                                                                           int P, float scale, int accumulate, TG *dtable,
+                                                                           const float *part)
+{
+    __shared__ float red[kJoinStrands][kJoinCols];
+    pdl_trigger();
+    pdl_wait();
+    const int piece = blockIdx.x, lo = piece * P, hi = min(rows, lo + P);
+    if (hi >= rows) return;
+    const int cur = tok[hi - 1];
+    if (tok[hi] != cur || cur >= vocab) return;              // no run leaves this piece
+    if (lo > 0 && tok[lo] == cur && tok[lo - 1] == cur) return;   // it started earlier
+    const int x = threadIdx.x % kJoinCols, y = threadIdx.x / kJoinCols, c = blockIdx.y * kJoinCols + x;
+    float sum = 0.f;
+    if (c < d) {
+        if (y == 0) sum = part[((size_t)piece * 2 + 1) * d + c];
+#pragma unroll 4
+        for (int q = piece + 1 + y; (size_t)q * P < (size_t)rows && tok[(size_t)q * P] == cur; q += kJoinStrands)
+            sum += part[(size_t)q * 2 * d + c];
+    }
+    red[y][x] = sum;
+    __syncthreads();
+    if (y == 0 && c < d) {
+        float t = red[0][x];
+#pragma unroll
+        for (int k = 1; k < kJoinStrands; ++k) t += red[k][x];
+        TG *o = dtable + (size_t)cur * d + c;
+        *o = from_f<TG>(accumulate ? fmaf(scale, t, to_f<TG>(*o)) : scale * t);
+    }
+}
+
+__global__ void __launch_bounds__(kSortThreads) fill_zero_kernel(void *p, size_t bytes)
+{
+    pdl_trigger();
+    pdl_wait();
+    fill_zero(p, bytes, 0);
+}
+
+template <class T, class TG>
+static cudaError_t run_sums(const EmbedGradArgs &a, const EmbedGradPlan &p, const int32_t *tok, const int32_t *idx,
+                            cudaStream_t s)
+{
+    float *part = (float *)(a.ws + p.o_part);
+    const bool vec = rows_aligned(a.dout, a.d) && rows_aligned(a.dtable, a.d);
+    const int cols = vec ? 8 * kRunThreads : 4 * kRunThreads;
+    const dim3 grid(p.pieces, (a.d + cols - 1) / cols);
+    cudaError_t e;
+    if (vec)
+        e = launch_k(run_sum_kernel<T, TG, 8>, grid, kRunThreads, (size_t)p.piece * 8, s, (const T *)a.dout, tok, idx,
+                     a.rows, a.d, a.vocab, p.piece, a.scale, a.accumulate, (TG *)a.dtable, part);
+    else
+        e = launch_k(run_sum_kernel<T, TG, 1>, grid, kRunThreads, (size_t)p.piece * 8, s, (const T *)a.dout, tok, idx,
+                     a.rows, a.d, a.vocab, p.piece, a.scale, a.accumulate, (TG *)a.dtable, part);
+    if (e != cudaSuccess || p.pieces < 2) return e;
+    return launch_k(run_join_kernel<TG>, dim3(p.pieces - 1, (a.d + kJoinCols - 1) / kJoinCols), kJoinCols * kJoinStrands,
+                    0, s, tok, a.rows, a.d, a.vocab, p.piece, a.scale, a.accumulate, (TG *)a.dtable, (const float *)part);
+}
+
+cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t s)
+{
+    const size_t bytes = (size_t)a.vocab * a.d * (a.dtable_dtype == ORTHRUS_BF16 ? 2 : 4);
+    const size_t zero_bytes = a.accumulate ? 0 : bytes;
+    // blocks that write zeros: two of 1024 threads per SM, fewer for small tables
+    const int fill = zero_bytes ? (int)std::min<size_t>(2 * 148, (zero_bytes + 16383) / 16384) : 0;
+    cudaError_t e;
+    if (a.rows == 0) {
+        if (!fill) return cudaSuccess;
+        return launch_k(fill_zero_kernel, fill, kSortThreads, 0, s, a.dtable, zero_bytes);
+    }
+    const EmbedGradPlan p = plan_embed_grad(a.rows, a.vocab, a.d);
+    int32_t *tok[2] = {(int32_t *)(a.ws + p.o_tok[0]), (int32_t *)(a.ws + p.o_tok[1])};
+    int32_t *idx[2] = {(int32_t *)(a.ws + p.o_idx[0]), (int32_t *)(a.ws + p.o_idx[1])};
+    int cur = 0;
+    if (a.rows <= kSortSmall) {
+        int n = 2, row_bits = 1;
+        while (n < a.rows) { n <<= 1; ++row_bits; }
+        int key_bits = 1;
+        while (key_bits < 31 && (a.vocab >> key_bits) != 0) ++key_bits;
+        // 32-bit keys while (token, row) fits below the padding key
+        if (key_bits + row_bits <= 31)
+            e = launch_k(sort_small_kernel<uint32_t>, 1 + fill, kSortThreads, (size_t)n * 4, s, a.ids, a.rows, a.vocab,
+                         row_bits, tok[0], idx[0], a.dtable, zero_bytes, a.err);
+        else {
+            e = cudaFuncSetAttribute(sort_small_kernel<uint64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kSortSmall * 8);
+            if (e != cudaSuccess) return e;
+            e = launch_k(sort_small_kernel<uint64_t>, 1 + fill, kSortThreads, (size_t)n * 8, s, a.ids, a.rows, a.vocab,
+                         row_bits, tok[0], idx[0], a.dtable, zero_bytes, a.err);
+        }
+        if (e != cudaSuccess) return e;
+    } else {
+        int *hist = (int *)(a.ws + p.o_hist);
+        const int32_t *st = a.ids, *si = nullptr;
+        for (int pass = 0; pass < p.digits; ++pass) {
+            const int shift = pass * p.digit_bits;
+            if (pass == 0)
+                e = launch_k(radix_hist_kernel<true>, p.tiles + 4 * fill, kRadixThreads, 0, s, st, a.rows, a.vocab,
+                             p.tiles, shift, p.digit_bits, hist, a.dtable, zero_bytes, a.err);
+            else
+                e = launch_k(radix_hist_kernel<false>, p.tiles, kRadixThreads, 0, s, st, a.rows, a.vocab, p.tiles, shift,
+                             p.digit_bits, hist, a.dtable, (size_t)0, a.err);
+            if (e != cudaSuccess) return e;
+            e = launch_k(radix_scan_kernel, 1, 1024, 0, s, hist, p.tiles << p.digit_bits);
+            if (e != cudaSuccess) return e;
+            if (pass == 0)
+                e = launch_k(radix_scatter_kernel<true>, p.tiles, kRadixThreads, 0, s, st, si, a.rows, a.vocab, p.tiles,
+                             shift, p.digit_bits, (const int *)hist, tok[0], idx[0]);
+            else
+                e = launch_k(radix_scatter_kernel<false>, p.tiles, kRadixThreads, 0, s, st, si, a.rows, a.vocab, p.tiles,
+                             shift, p.digit_bits, (const int *)hist, tok[pass & 1], idx[pass & 1]);
+            if (e != cudaSuccess) return e;
+            cur = pass & 1;
+            st = tok[cur];
+            si = idx[cur];
+        }
+    }
+    const bool ib = a.dout_dtype == ORTHRUS_BF16, ob = a.dtable_dtype == ORTHRUS_BF16;
+    if (ib)
+        return ob ? run_sums<bf16, bf16>(a, p, tok[cur], idx[cur], s) : run_sums<bf16, float>(a, p, tok[cur], idx[cur], s);
+    return ob ? run_sums<float, bf16>(a, p, tok[cur], idx[cur], s) : run_sums<float, float>(a, p, tok[cur], idx[cur], s);
+}
+
+// ---------------------------------------------------------------- RMSNorm
+// Forward: y = x r g with r = (mean x^2 + eps)^-1/2, in fp32.  G threads per
+// row; the first J chunks of a thread stay in registers between the sum and
+// the output, longer rows are read again.
+constexpr int kNormRowsThreads = 256;
+
+// Sum over the G threads of a row: a warp, or the whole block.
+template <int G, int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float *red)
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    if (G == 32) return;
+    constexpr int W = G / 32;
+    const int gi = threadIdx.x / G, w = (threadIdx.x % G) >> 5, lane = threadIdx.x & 31;
+    float *r = red + gi * W * N;
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[w * N + i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) t += r[k * N + i];
+        v[i] = t;
+    }
+}
+
+template <class TX, class T, int VEC, int G>
+__global__ void __launch_bounds__(kNormRowsThreads) norm_rows_kernel(const TX *x, const T *gain, T *y, int rows, int d,
+                                                                     float eps)
+{
+    constexpr int J = VEC == 8 ? 4 : 8;
+    __shared__ float red[kNormRowsThreads / 32];
+    pdl_trigger();
+    pdl_wait();
+    const int row = blockIdx.x * (kNormRowsThreads / G) + threadIdx.x / G, t = threadIdx.x % G;
+    if (row >= rows) return;   // (whole warps; with G = 256 the whole block)
+    const TX *xr = x + (size_t)row * d;
+    const int nc = d / VEC;
+    float v[J][VEC], ss[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int c = t + j * G;
+        if (c < nc) RowVec<TX, VEC>::load(xr + (size_t)c * VEC, v[j]);
+        else
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) v[j][e] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) ss[0] = fmaf(v[j][e], v[j][e], ss[0]);
+    for (int c = t + J * G; c < nc; c += G) {
+        float u[VEC];
+        RowVec<TX, VEC>::load(xr + (size_t)c * VEC, u);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) ss[0] = fmaf(u[e], u[e], ss[0]);
+    }
+    group_sum<G, 1>(ss, red);
+    const float r = 1.0f / sqrtf(ss[0] / (float)d + eps);
+    T *yr = y + (size_t)row * d;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int c = t + j * G;
+        if (c >= nc) continue;
+        float g[VEC], o[VEC];
+        RowVec<T, VEC>::load(gain + (size_t)c * VEC, g);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = v[j][e] * r * g[e];
+        RowVec<T, VEC>::store(yr + (size_t)c * VEC, o);
+    }
+    for (int c = t + J * G; c < nc; c += G) {
+        float u[VEC], g[VEC], o[VEC];
+        RowVec<TX, VEC>::load(xr + (size_t)c * VEC, u);
+        RowVec<T, VEC>::load(gain + (size_t)c * VEC, g);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) o[e] = u[e] * r * g[e];
+        RowVec<T, VEC>::store(yr + (size_t)c * VEC, o);
+    }
+}
+
+template <class TX, class T> static cudaError_t norm_rows_t(const NormArgs &a, cudaStream_t s)
+{
+    const bool vec = rows_aligned(a.x, a.d) && rows_aligned(a.gain, a.d) && rows_aligned(a.out, a.d);
+    auto go = [&](auto kernel, int G) {
+        const int per = kNormRowsThreads / G;
+        return launch_k(kernel, (a.rows + per - 1) / per, kNormRowsThreads, 0, s, (const TX *)a.x, (const T *)a.gain,
+                        (T *)a.out, a.rows, a.d, a.eps);
+    };
+    // a warp per row while the row fits its registers
+    if (vec) return a.d <= 1024 ? go(norm_rows_kernel<TX, T, 8, 32>, 32) : go(norm_rows_kernel<TX, T, 8, 256>, 256);
+    return a.d <= 256 ? go(norm_rows_kernel<TX, T, 1, 32>, 32) : go(norm_rows_kernel<TX, T, 1, 256>, 256);
+}
+
+cudaError_t launch_norm_rows(const NormArgs &a, cudaStream_t s)
+{
+    const bool xb = a.x_dtype == ORTHRUS_BF16, yb = a.dtype == ORTHRUS_BF16;
+    if (xb) return yb ? norm_rows_t<bf16, bf16>(a, s) : cudaErrorNotSupported;
+    return yb ? norm_rows_t<float, bf16>(a, s) : norm_rows_t<float, float>(a, s);
+}
+
+// Gradient.  With u = g dy, A = sum x^2, B = sum u x over a row and
+// r = (A/d + eps)^-1/2:
+//     dx = r u - r^3 (B/d) x,     dgain = sum over rows of dy x r.
+// One pass: a row's x and dy are read once into registers, both sums are
+// reduced together, dx is written, and dgain's columns stay in the thread's
+// registers over all rows the block takes; each block leaves its column sums
+// in the workspace and a second kernel adds the blocks up in a fixed order.
+constexpr int kNgThreads = 512;
+constexpr int kNgMaxCols = 8192;     // longest row the register path holds
+constexpr int kNgBlocks = 2 * 148;   // blocks: two per SM
+
+template <class TX, class T, int VEC, int G, int J>
+__global__ void __launch_bounds__(kNgThreads) norm_grad_kernel(const TX *x, const T *gain, const T *dy, TX *dx, int rows,
+                                                               int d, float eps, float *part)
+{
+    constexpr int R = kNgThreads / G;   // rows of a block at a time
+    __shared__ float red[2][2 * kNgThreads / 32];
+    __shared__ float comb[R > 1 ? kNgThreads * VEC : 1];
+    pdl_trigger();
+    const int gi = threadIdx.x / G, t = threadIdx.x % G, nc = d / VEC;
+    pdl_wait();
+    float g[J][VEC], acc[J][VEC];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int c = t + j * G;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) { acc[j][e] = 0.f; g[j][e] = 0.f; }
+        if (c < nc) RowVec<T, VEC>::load(gain + (size_t)c * VEC, g[j]);
+    }
+    int flip = 0;
+    for (int r0 = blockIdx.x * R; r0 < rows; r0 += gridDim.x * R, flip ^= 1) {
+        const int row = r0 + gi;
+        const bool live = row < rows;
+        float xv[J][VEC], u[J][VEC], s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int c = t + j * G;
+            if (live && c < nc) {
+                RowVec<TX, VEC>::load(x + (size_t)row * d + (size_t)c * VEC, xv[j]);
+                RowVec<T, VEC>::load(dy + (size_t)row * d + (size_t)c * VEC, u[j]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) { xv[j][e] = 0.f; u[j][e] = 0.f; }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                s[0] = fmaf(xv[j][e], xv[j][e], s[0]);
+                s[1] = fmaf(u[j][e] * g[j][e], xv[j][e], s[1]);
+            }
+        // (two buffers: a block reads one while the next row writes the other)
+        group_sum<G, 2>(s, red[flip]);
+        const float r = 1.0f / sqrtf(s[0] / (float)d + eps), k = r * r * r * (s[1] / (float)d);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int c = t + j * G;
+            if (!live || c >= nc) continue;
+            float o[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                o[e] = r * (u[j][e] * g[j][e]) - k * xv[j][e];
+                acc[j][e] = fmaf(u[j][e] * xv[j][e], r, acc[j][e]);
+            }
+            RowVec<TX, VEC>::store(dx + (size_t)row * d + (size_t)c * VEC, o);
+        }
+    }
+    float *p = part + (size_t)blockIdx.x * d;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int c = t + j * G;
+        if (R > 1) {   // the block's row groups, in order
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) comb[threadIdx.x * VEC + e] = acc[j][e];
+            __syncthreads();
+            if (gi == 0)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e)
+                    for (int q = 1; q < R; ++q) acc[j][e] += comb[(q * G + t) * VEC + e];
+        }
+        if (gi == 0 && c < nc)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) p[(size_t)c * VEC + e] = acc[j][e];
+    }
+}
+
+// Rows longer than kNgMaxCols: row statistics and dx by one block per row
+// (x and dy are read twice), dgain by blocks of columns over strips of rows.
+template <class TX, class T>
+__global__ void __launch_bounds__(kNgThreads) norm_grad_long_kernel(const TX *x, const T *gain, const T *dy, TX *dx,
+                                                                    int rows, int d, float eps, float *rstd)
+{
+    __shared__ float red[2 * kNgThreads / 32];
+    pdl_trigger();
+    pdl_wait();
+    const int row = blockIdx.x;
+    const TX *xr = x + (size_t)row * d;
+    const T *yr = dy + (size_t)row * d;
+    float s[2] = {0.f, 0.f};
+    for (int c = threadIdx.x; c < d; c += kNgThreads) {
+        const float xv = to_f<TX>(xr[c]);
+        s[0] = fmaf(xv, xv, s[0]);
+        s[1] = fmaf(to_f<T>(yr[c]) * to_f<T>(gain[c]), xv, s[1]);
+    }
+    group_sum<kNgThreads, 2>(s, red);
+    const float r = 1.0f / sqrtf(s[0] / (float)d + eps), k = r * r * r * (s[1] / (float)d);
+    if (threadIdx.x == 0) rstd[row] = r;
+    for (int c = threadIdx.x; c < d; c += kNgThreads) {
+        const float xv = to_f<TX>(xr[c]);
+        dx[(size_t)row * d + c] = from_f<TX>(r * (to_f<T>(yr[c]) * to_f<T>(gain[c])) - k * xv);
+    }
+}
+
+template <class TX, class T>
+__global__ void __launch_bounds__(256) norm_grad_cols_kernel(const TX *x, const T *dy, const float *rstd, int rows, int d,
+                                                             float *part)
+{
+    pdl_trigger();
+    pdl_wait();
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= d) return;
+    float acc = 0.f;
+    for (int r = blockIdx.y; r < rows; r += gridDim.y)
+        acc = fmaf(to_f<T>(dy[(size_t)r * d + c]) * to_f<TX>(x[(size_t)r * d + c]), rstd[r], acc);
+    part[(size_t)blockIdx.y * d + c] = acc;
+}
+
+// dgain[c] = sum over blocks of part[block][c], 8 strands joined in order
+__global__ void __launch_bounds__(256) dgain_kernel(const float *part, int blocks, int d, float *dgain)
+{
+    __shared__ float red[8][32];
+    pdl_trigger();
+    pdl_wait();
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+    float s = 0.f;
+    if (c < d)
+#pragma unroll 8
+        for (int b = y; b < blocks; b += 8) s += part[(size_t)b * d + c];
+    red[y][x] = s;
+    __syncthreads();
+    if (y == 0 && c < d) {
+        float t = red[0][x];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) t += red[k][x];
+        dgain[c] = t;
+    }
+}
+
+size_t norm_grad_workspace(int rows, int d)
+{
+    WsPlan w;
+    w.take((size_t)kNgBlocks * d * 4);
+    w.take(d > kNgMaxCols ? (size_t)rows * 4 : 0);
+    return w.total;
+}
+
+template <class TX, class T> static cudaError_t norm_grad_t(const NormArgs &a, cudaStream_t s)
+{
+    const bool vec = rows_aligned(a.x, a.d) && rows_aligned(a.gain, a.d) && rows_aligned(a.dy, a.d) &&
+                     rows_aligned(a.out, a.d);
+    float *part = (float *)a.ws;
+    int blocks = 0;
+    cudaError_t e;
+    if (a.d > kNgMaxCols) {
+        WsPlan w;
+        w.take((size_t)kNgBlocks * a.d * 4);
+        float *rstd = (float *)(a.ws + w.take((size_t)a.rows * 4));
+        e = launch_k(norm_grad_long_kernel<TX, T>, a.rows, kNgThreads, 0, s, (const TX *)a.x, (const T *)a.gain,
+                     (const T *)a.dy, (TX *)a.out, a.rows, a.d, a.eps, rstd);
+        if (e != cudaSuccess) return e;
+        blocks = std::min(32, a.rows);
+        e = launch_k(norm_grad_cols_kernel<TX, T>, dim3((a.d + 255) / 256, blocks), 256, 0, s, (const TX *)a.x,
+                     (const T *)a.dy, (const float *)rstd, a.rows, a.d, part);
+    } else {
+        auto go = [&](auto kernel, int G) {
+            const int R = kNgThreads / G;
+            blocks = std::min(kNgBlocks, (a.rows + R - 1) / R);
+            return launch_k(kernel, blocks, kNgThreads, 0, s, (const TX *)a.x, (const T *)a.gain, (const T *)a.dy,
+                            (TX *)a.out, a.rows, a.d, a.eps, part);
+        };
+        // threads per row: as few as hold the row in registers
+        if (vec)
+            e = a.d <= 512 ? go(norm_grad_kernel<TX, T, 8, 32, 2>, 32)
+                : a.d <= 2048 ? go(norm_grad_kernel<TX, T, 8, 128, 2>, 128)
+                              : go(norm_grad_kernel<TX, T, 8, 512, 2>, 512);
+        else
+            e = a.d <= 512 ? go(norm_grad_kernel<TX, T, 1, 32, 16>, 32)
+                : a.d <= 2048 ? go(norm_grad_kernel<TX, T, 1, 128, 16>, 128)
+                              : go(norm_grad_kernel<TX, T, 1, 512, 16>, 512);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_k(dgain_kernel, (a.d + 31) / 32, 256, 0, s, (const float *)part, blocks, a.d, a.dgain);
+}
+
+cudaError_t launch_norm_grad(const NormArgs &a, cudaStream_t s)
+{
+    if (a.rows == 0) return launch_k(dgain_kernel, (a.d + 31) / 32, 256, 0, s, (const float *)nullptr, 0, a.d, a.dgain);
+    const bool xb = a.x_dtype == ORTHRUS_BF16, yb = a.dtype == ORTHRUS_BF16;
+    if (xb) return yb ? norm_grad_t<bf16, bf16>(a, s) : cudaErrorNotSupported;
+    return yb ? norm_grad_t<float, bf16>(a, s) : norm_grad_t<float, float>(a, s);
+}
+
+}  // namespace orthrus

@@ -1,0 +1,418 @@
+// Losses through the shared LM head without keeping the logits: the cross
+// entropy of one token id per row with its gradients, and the gradient of
+// the forward KL(p_AR || p_diff) (paper notes §3.3).  With z = W h:
+//     CE   lse = log sum_v exp z_v,  loss = lse - z_t,
+//          dz_v = g (exp(z_v - lse) - [v = t])
+//     KL   dz_v = g (softmax(W h_diff)_v - softmax(W h_AR)_v)
+//     dh = dz W,   dW = dz^T h.
+// The forward pass keeps a maximum and a sum of exponentials per (row,
+// vocabulary tile).  The gradient goes over the vocabulary in pieces: a
+// piece's dz is made from recomputed logits and the row's log-sum-exp, and
+// used for its part of dh and its rows of dW before the next piece takes its
+// place, so the scratch does not grow with the vocabulary.
+//
+// This file: the plan over the workspace, the kernels every path shares, and
+// the SIMT path (fp32, and bf16 rows that TMA cannot address).  The tensor-core
+// path of bf16 is in vocab_loss_tc.cu.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "train.h"
+
+namespace orthrus {
+
+// ---------------------------------------------------------------- tiles
+constexpr int kSt = 64;            // rows and columns of a SIMT tile
+constexpr int kStK = 16;           // k per step
+constexpr int kStThreads = 256;
+constexpr int kStFlush = 8;        // steps per partial sum (128 products)
+
+// A strided operand: element (row, k).
+template <class T> struct Operand {
+    const T *p;
+    size_t row_stride, k_stride;
+    int rows;
+    __device__ __forceinline__ float at(int r, size_t k) const { return to_f<T>(p[r * row_stride + k * k_stride]); }
+};
+
+// acc[i][j] = sum over k in [k0, k1) of A(m0 + 4 ty + i, k) B(n0 + 4 tx + j, k).
+// Sums of 128 products are added up separately, so the rounding error grows
+// with the root of K / 128, not of K.  AK / BK: the operand's k is contiguous.
+template <class TA, class TB, bool AK, bool BK>
+__device__ void simt_tile(const Operand<TA> &A, const Operand<TB> &B, int m0, int n0, size_t k0, size_t k1,
+                          float (&acc)[4][4], float (&sa)[kStK][kSt + 4], float (&sb)[kStK][kSt + 4])
+{
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float part[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) { acc[i][j] = 0.f; part[i][j] = 0.f; }
+    float ra[4], rb[4];
+    auto fetch = [&](size_t k) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {   // consecutive threads walk the contiguous axis
+            const int e = threadIdx.x + q * kStThreads;
+            const int ar = AK ? e / kStK : e % kSt, ak = AK ? e % kStK : e / kSt;
+            const int br = BK ? e / kStK : e % kSt, bk = BK ? e % kStK : e / kSt;
+            ra[q] = m0 + ar < A.rows && k + ak < k1 ? A.at(m0 + ar, k + ak) : 0.f;
+            rb[q] = n0 + br < B.rows && k + bk < k1 ? B.at(n0 + br, k + bk) : 0.f;
+        }
+    };
+    fetch(k0);
+    int step = 0;
+    for (size_t k = k0; k < k1; k += kStK) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int e = threadIdx.x + q * kStThreads;
+            if (AK) sa[e % kStK][e / kStK] = ra[q]; else sa[e / kSt][e % kSt] = ra[q];
+            if (BK) sb[e % kStK][e / kStK] = rb[q]; else sb[e / kSt][e % kSt] = rb[q];
+        }
+        __syncthreads();
+        if (k + kStK < k1) fetch(k + kStK);
+#pragma unroll
+        for (int kk = 0; kk < kStK; ++kk) {
+            const float4 a = *(const float4 *)&sa[kk][ty * 4], b = *(const float4 *)&sb[kk][tx * 4];
+            const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) part[i][j] = fmaf(av[i], bv[j], part[i][j]);
+        }
+        __syncthreads();
+        if (++step % kStFlush == 0 || k + kStK >= k1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) { acc[i][j] += part[i][j]; part[i][j] = 0.f; }
+    }
+}
+
+// The shift of a sum of exponentials whose maximum is m: 0 where every term is
+// exp(-inf) (a NaN among them still makes the sum a NaN).
+__device__ __forceinline__ float exp_shift(float m) { return m == -INFINITY ? 0.f : m; }
+
+struct StSmem {
+    float a[kStK][kSt + 4], b[kStK][kSt + 4];
+};
+
+// Forward: per (64-id tile, row) maximum and sum of exponentials, and the
+// logit of the row's target.
+template <class T>
+__global__ void __launch_bounds__(kStThreads) ce_tile_simt(const T *h, const T *w, const int32_t *targets, int N, int d,
+                                                           int V, float2 *rec, float *zt)
+{
+    __shared__ __align__(16) StSmem sm;
+    __shared__ float z[kSt][kSt + 1];
+    pdl_trigger();
+    pdl_wait();
+    const int m0 = blockIdx.y * kSt, n0 = blockIdx.x * kSt;
+    float acc[4][4];
+    const Operand<T> A{h, (size_t)d, 1, N}, B{w, (size_t)d, 1, V};
+    simt_tile<T, T, true, true>(A, B, m0, n0, 0, d, acc, sm.a, sm.b);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[ty * 4 + i][tx * 4 + j] = acc[i][j];
+    __syncthreads();
+    const int r = threadIdx.x >> 2, q = threadIdx.x & 3, row = m0 + r, nv = min(kSt, V - n0);
+    float m = -INFINITY, s = 0.f;
+    for (int c = q; c < nv; c += 4) m = fmaxf(m, z[r][c]);
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const float sh = exp_shift(m);
+    for (int c = q; c < nv; c += 4) s += expf(z[r][c] - sh);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    if (q == 0 && row < N) {
+        rec[(size_t)blockIdx.x * N + row] = make_float2(m, s);
+        const int t = targets[row];
+        if (t >= n0 && t < n0 + nv) zt[row] = z[r][t - n0];
+    }
+}
+
+// lse and loss from the tiles' records: 32 rows x 8 strands of tiles.
+__global__ void __launch_bounds__(256) ce_finalize_kernel(const float2 *rec, const float *zt, const int32_t *targets,
+                                                          int n_tiles, int N, int V, float *loss, float *lse,
+                                                          unsigned *err)
+{
+    __shared__ float sm[8][32], ss[8][32];
+    pdl_trigger();
+    pdl_wait();
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, row = blockIdx.x * 32 + x;
+    float m = -INFINITY, s = 0.f;
+    if (row < N) {
+#pragma unroll 4
+        for (int i = y; i < n_tiles; i += 8) {
+            const float2 v = rec[(size_t)i * N + row];
+            const float mn = fmaxf(m, v.x);
+            const float sh = exp_shift(mn);
+            s = (m == mn ? s : s * expf(m - sh)) + v.y * expf(v.x - sh);
+            m = mn;
+        }
+    }
+    sm[y][x] = m;
+    ss[y][x] = s;
+    __syncthreads();
+    if (y || row >= N) return;
+    float M = sm[0][x], S = 0.f;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) M = fmaxf(M, sm[k][x]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (ss[k][x] != 0.f) S += ss[k][x] * expf(sm[k][x] - exp_shift(M));
+    const float L = M + logf(S);
+    const int t = targets[row];
+    lse[row] = L;
+    if (t >= V && err) raise_err(err, ORTHRUS_DEVERR_TOKEN);
+    if (t < 0 || t >= V) { loss[row] = 0.f; return; }
+    if (!isfinite(L) && err) raise_err(err, ORTHRUS_DEVERR_NONFINITE);
+    loss[row] = L - zt[row];
+}
+
+// dz of one piece [v0, v0 + Vp) of the vocabulary, fp32.  A row whose
+// upstream gradient is zero, or that has no target, gets exact zeros
+// whatever its hidden row holds.
+template <class T, bool KL>
+__global__ void __launch_bounds__(kStThreads) dz_tile_simt(LossArgs a, int v0, int Vp, float *dz)
+{
+    __shared__ __align__(16) StSmem sm;
+    pdl_trigger();
+    pdl_wait();
+    const int m0 = blockIdx.y * kSt, n0 = v0 + blockIdx.x * kSt, d = a.d;
+    const int vend = min(a.V, v0 + Vp);
+    float z[4][4], z2[4][4];
+    const Operand<T> A{(const T *)a.h, (size_t)d, 1, a.N}, B{(const T *)a.w, (size_t)d, 1, a.V};
+    simt_tile<T, T, true, true>(A, B, m0, n0, 0, d, z, sm.a, sm.b);
+    if (KL) {
+        const Operand<T> A2{(const T *)a.h2, (size_t)d, 1, a.N};
+        simt_tile<T, T, true, true>(A2, B, m0, n0, 0, d, z2, sm.a, sm.b);
+    }
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = m0 + ty * 4 + i;
+        if (row >= a.N) continue;
+        const float lse = a.lse_in[row];
+        float g = a.g[row], lse2 = 0.f;
+        int t = -1;
+        if (KL) lse2 = a.lse2_in[row];
+        else {
+            t = a.targets[row];
+            if (t >= a.V && tx == 0 && blockIdx.x == 0 && a.err) raise_err(a.err, ORTHRUS_DEVERR_TOKEN);
+            if (t < 0 || t >= a.V) g = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int v = n0 + tx * 4 + j;
+            if (v >= vend) continue;
+            float x;
+            if (KL) x = expf(z2[i][j] - lse2) - expf(z[i][j] - lse);
+            else x = expf(z[i][j] - lse) - (v == t ? 1.f : 0.f);
+            dz[(size_t)row * Vp + (v - v0)] = g == 0.f ? 0.f : g * x;
+        }
+    }
+}
+
+// C = A B^T over k in the split's share of [0, K): dh parts (fp32, added to
+// what earlier pieces left) and dW rows (T).
+struct GradGemm {
+    int M, N, K, splits;      // C is [M][N]
+    float *part;              // [splits][M][N], or null: write out
+    int add;                  // add to part
+    void *out;
+};
+template <class TA, class TB, bool AK, class TO>
+__global__ void __launch_bounds__(kStThreads) grad_gemm_simt(Operand<TA> A, Operand<TB> B, GradGemm g)
+{
+    __shared__ __align__(16) StSmem sm;
+    pdl_trigger();
+    pdl_wait();
+    const int m0 = blockIdx.y * kSt, n0 = blockIdx.x * kSt, sp = blockIdx.z;
+    const size_t per = (((size_t)g.K + g.splits - 1) / g.splits + kStK - 1) / kStK * kStK;
+    const size_t k0 = min((size_t)g.K, per * sp), k1 = min((size_t)g.K, k0 + per);
+    float acc[4][4];
+    simt_tile<TA, TB, AK, false>(A, B, m0, n0, k0, k1, acc, sm.a, sm.b);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int m = m0 + ty * 4 + i;
+        if (m >= g.M) continue;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int n = n0 + tx * 4 + j;
+            if (n >= g.N) continue;
+            const size_t o = (size_t)m * g.N + n;
+            if (g.part) {
+                float *p = g.part + (size_t)sp * g.M * g.N + o;
+                *p = g.add ? *p + acc[i][j] : acc[i][j];
+            } else {
+                ((TO *)g.out)[o] = from_f<TO>(acc[i][j]);
+            }
+        }
+    }
+}
+
+// out = sum of the splits' parts, in order, rounded once.
+template <class T>
+__global__ void __launch_bounds__(256) part_sum_kernel(const float *part, int splits, size_t n, T *out)
+{
+    pdl_trigger();
+    pdl_wait();
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
+        float s = part[i];
+        for (int k = 1; k < splits; ++k) s += part[(size_t)k * n + i];
+        out[i] = from_f<T>(s);
+    }
+}
+
+cudaError_t launch_part_sum(const float *part, int splits, size_t n, void *out, int dtype, cudaStream_t s)
+{
+    const int grid = (int)std::min<size_t>((n + 255) / 256, 8 * 148);
+    if (dtype == ORTHRUS_BF16) return launch_k(part_sum_kernel<bf16>, grid, 256, 0, s, part, splits, n, (bf16 *)out);
+    return launch_k(part_sum_kernel<float>, grid, 256, 0, s, part, splits, n, (float *)out);
+}
+
+// The hidden rows with the rows that take no part zeroed, for dW = dz^T h: a
+// padding row's dz is zero, but zero times a NaN or an infinity in its
+// hidden row would not be.
+template <class T>
+__global__ void __launch_bounds__(256) clean_rows_kernel(const T *h, const int32_t *targets, const float *g, int N, int d,
+                                                         int V, T *out)
+{
+    pdl_trigger();
+    pdl_wait();
+    const int row = blockIdx.x;
+    const int t = targets[row];
+    const bool live = t >= 0 && t < V && g[row] != 0.f;
+    const T *src = h + (size_t)row * d;
+    T *dst = out + (size_t)row * d;
+    constexpr int E = 16 / (int)sizeof(T);
+    if (d % E == 0 && (((uintptr_t)src | (uintptr_t)dst) & 15) == 0) {
+        for (int i = threadIdx.x; i < d / E; i += 256)
+            ((uint4 *)dst)[i] = live ? ((const uint4 *)src)[i] : make_uint4(0, 0, 0, 0);
+    } else {
+        for (int i = threadIdx.x; i < d; i += 256) dst[i] = live ? src[i] : from_f<T>(0.f);
+    }
+}
+
+cudaError_t launch_clean_rows(const LossArgs &a, void *out, cudaStream_t s)
+{
+    if (a.dtype == ORTHRUS_BF16)
+        return launch_k(clean_rows_kernel<bf16>, a.N, 256, 0, s, (const bf16 *)a.h, a.targets, a.g, a.N, a.d, a.V,
+                        (bf16 *)out);
+    return launch_k(clean_rows_kernel<float>, a.N, 256, 0, s, (const float *)a.h, a.targets, a.g, a.N, a.d, a.V,
+                    (float *)out);
+}
+
+__global__ void __launch_bounds__(1024) zero_kernel(void *p, size_t bytes)
+{
+    pdl_trigger();
+    pdl_wait();
+    const size_t n16 = ((uintptr_t)p & 15) == 0 ? bytes / 16 : 0;
+    const size_t t = (size_t)blockIdx.x * 1024 + threadIdx.x, n = (size_t)gridDim.x * 1024;
+    for (size_t i = t; i < n16; i += n) ((uint4 *)p)[i] = make_uint4(0, 0, 0, 0);
+    for (size_t i = n16 * 16 + t * 2; i < bytes; i += n * 2) *(uint16_t *)((char *)p + i) = 0;
+}
+
+// ---------------------------------------------------------------- plans
+struct SimtPlan {
+    size_t total, o_dz, o_part, o_h;
+    int piece, splits;
+};
+static SimtPlan plan_simt(int N, int d, int V, int es, int want_dw)
+{
+    SimtPlan p{};
+    WsPlan w;
+    // a piece's dz stays within 64 MiB
+    const size_t cap = std::max<size_t>(kSt, ((size_t)64 << 20) / (4 * (size_t)std::max(N, 1)) / kSt * kSt);
+    p.piece = (int)std::min<size_t>(cap, ((size_t)V + kSt - 1) / kSt * kSt);
+    // dh has few tiles at small N and d: its k axis (the piece) is cut until
+    // the blocks cover the SMs about twice, in shares of at least 256 ids
+    const long tiles = (long)((N + kSt - 1) / kSt) * ((d + kSt - 1) / kSt);
+    p.splits = (int)std::max<long>(1, std::min<long>({(2 * 148 + tiles - 1) / tiles, (p.piece + 255) / 256, 32L}));
+    p.o_dz = w.take((size_t)N * p.piece * 4);
+    p.o_part = w.take((size_t)p.splits * N * d * 4);
+    p.o_h = w.take(want_dw ? (size_t)N * d * es : 0);
+    p.total = w.total;
+    return p;
+}
+
+size_t loss_fwd_workspace(int N, int d, int V, int dtype)
+{
+    WsPlan w;
+    w.take((size_t)((V + kSt - 1) / kSt) * N * sizeof(float2));
+    w.take((size_t)N * 4);
+    return w.total;
+}
+
+size_t loss_grad_workspace(int N, int d, int V, int dtype, int want_dw, int kl)
+{
+    return plan_simt(N, d, V, dtype == ORTHRUS_BF16 ? 2 : 4, want_dw).total;
+}
+
+// ---------------------------------------------------------------- launches
+template <class T> static cudaError_t loss_fwd_simt(const LossArgs &a, cudaStream_t s)
+{
+    WsPlan w;
+    const int nt = (a.V + kSt - 1) / kSt;
+    float2 *rec = (float2 *)(a.ws + w.take((size_t)nt * a.N * sizeof(float2)));
+    float *zt = (float *)(a.ws + w.take((size_t)a.N * 4));
+    cudaError_t e = launch_k(ce_tile_simt<T>, dim3(nt, (a.N + kSt - 1) / kSt), kStThreads, 0, s, (const T *)a.h,
+                             (const T *)a.w, a.targets, a.N, a.d, a.V, rec, zt);
+    if (e != cudaSuccess) return e;
+    return launch_k(ce_finalize_kernel, (a.N + 31) / 32, 256, 0, s, (const float2 *)rec, (const float *)zt, a.targets, nt,
+                    a.N, a.V, a.loss, a.lse, a.err);
+}
+
+template <class T> static cudaError_t loss_grad_simt(const LossArgs &a, cudaStream_t s)
+{
+    const SimtPlan p = plan_simt(a.N, a.d, a.V, (int)sizeof(T), a.dw != nullptr);
+    float *dz = (float *)(a.ws + p.o_dz), *part = (float *)(a.ws + p.o_part);
+    T *hc = (T *)(a.ws + p.o_h);
+    const unsigned mt = (a.N + kSt - 1) / kSt, dt = (a.d + kSt - 1) / kSt;
+    cudaError_t e;
+    if (a.dw && (e = launch_clean_rows(a, hc, s)) != cudaSuccess) return e;
+    for (int v0 = 0; v0 < a.V; v0 += p.piece) {
+        const int nv = std::min(p.piece, a.V - v0);
+        const dim3 gz((nv + kSt - 1) / kSt, mt);
+        e = a.kl ? launch_k(dz_tile_simt<T, true>, gz, kStThreads, 0, s, a, v0, p.piece, dz)
+                 : launch_k(dz_tile_simt<T, false>, gz, kStThreads, 0, s, a, v0, p.piece, dz);
+        if (e != cudaSuccess) return e;
+        const Operand<float> A{dz, (size_t)p.piece, 1, a.N};
+        const Operand<T> B{(const T *)a.w + (size_t)v0 * a.d, 1, (size_t)a.d, a.d};
+        GradGemm g{};
+        g.M = a.N; g.N = a.d; g.K = nv; g.splits = p.splits; g.part = part; g.add = v0 > 0;
+        e = launch_k(grad_gemm_simt<float, T, true, T>, dim3(dt, mt, p.splits), kStThreads, 0, s, A, B, g);
+        if (e != cudaSuccess) return e;
+        if (!a.dw) continue;
+        const Operand<float> At{dz, 1, (size_t)p.piece, nv};
+        const Operand<T> Bh{hc, 1, (size_t)a.d, a.d};
+        GradGemm gw{};
+        gw.M = nv; gw.N = a.d; gw.K = a.N; gw.splits = 1; gw.out = (T *)a.dw + (size_t)v0 * a.d;
+        e = launch_k(grad_gemm_simt<float, T, false, T>, dim3(dt, (nv + kSt - 1) / kSt, 1), kStThreads, 0, s, At, Bh, gw);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_part_sum(part, p.splits, (size_t)a.N * a.d, a.dh, a.dtype, s);
+}
+
+cudaError_t launch_loss_fwd(const LossArgs &a, cudaStream_t s)
+{
+    if (a.N == 0) return cudaSuccess;
+    return a.dtype == ORTHRUS_BF16 ? loss_fwd_simt<bf16>(a, s) : loss_fwd_simt<float>(a, s);
+}
+
+cudaError_t launch_loss_grad(const LossArgs &a, cudaStream_t s)
+{
+    if (a.N == 0) {   // no rows: dW is zero
+        if (!a.dw) return cudaSuccess;
+        return launch_k(zero_kernel, 2 * 148, 1024, 0, s, a.dw,
+                        (size_t)a.V * a.d * (a.dtype == ORTHRUS_BF16 ? 2 : 4));
+    }
+    return a.dtype == ORTHRUS_BF16 ? loss_grad_simt<bf16>(a, s) : loss_grad_simt<float>(a, s);
+}
+
+}  // namespace orthrus

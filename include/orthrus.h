@@ -25,7 +25,10 @@
  * orthrus_tree_build / orthrus_verify_tree / orthrus_tree_commit (tree
  * verification over the draft's marginals, §7.5, §9.6), and
  * orthrus_adaptive_len / orthrus_commit_adaptive (a verify length set by the
- * draft rows' entropies, §7.4, §9.6).
+ * draft rows' entropies, §7.4, §9.6), and the training-side operators with
+ * their gradients, which need no context: orthrus_embed_rows /
+ * orthrus_embed_grad, orthrus_rmsnorm / orthrus_rmsnorm_grad,
+ * orthrus_ce_lm_head / orthrus_ce_lm_head_grad, orthrus_kl_lm_head_grad.
  *
  * Conventions for every entry point:
  *   - Every pointer to tensor data is a DEVICE pointer owned by the caller
@@ -497,6 +500,114 @@ orthrus_status_t orthrus_tree_commit(orthrus_ctx_t *ctx, const orthrus_kv_t *kv,
                                      const int32_t *parent, const int32_t *token, const int32_t *n_rows,
                                      const int32_t *g, int32_t *n_out, int32_t *emit, int32_t *anchor,
                                      void *stream);
+
+/*
+ * Training-side operators at the two ends of the model: the token embedding,
+ * the RMSNorm in front of the head, and the losses through the shared LM
+ * head, each with its gradient.  A distillation step of the diffusion view
+ * (paper notes §3.3) is orthrus_embed_rows over the packed blocks, the
+ * layers, orthrus_rmsnorm, orthrus_kl_lm_head (or orthrus_ce_lm_head on the
+ * data's own tokens), and the gradients in the opposite order.
+ *
+ * They need no context: shapes and device pointers come with the call, and
+ * scratch is a workspace of the caller (device, 256-byte aligned, its size
+ * from the call's *_workspace function; contents need not be kept or
+ * cleared).  Common to all:
+ *   - dtype arguments are orthrus_dtype_t.  Tensors are dense, row-major and
+ *     aligned to their element size; buffers of one call must not overlap.
+ *     Rows of a multiple of 8 elements with 16-byte aligned buffers take
+ *     16-byte accesses (and, for the bf16 losses, the tensor cores); every
+ *     other shape runs too, slower.
+ *   - rows may be 0 (tensor pointers of that many rows may then be NULL).
+ *     rows and vocab are at most 4,000,000 and hidden at most 65,536
+ *     (ORTHRUS_ERR_CAPACITY); a workspace that is too small is
+ *     ORTHRUS_ERR_CAPACITY.
+ *   - everything is enqueued on `stream`, on the current device; nothing is
+ *     allocated or synchronised.  Calls may be captured; two calls may run at
+ *     the same time on one GPU when their workspaces and outputs differ.
+ *   - dev_err: device uint32 of the caller or NULL.  ORTHRUS_DEVERR_* bits of
+ *     problems that only the device can see are ORed into it; it is never
+ *     cleared here.
+ *   - Sums are held in fp32 and taken in an order that the shapes alone fix,
+ *     so a call repeated on the same inputs gives the same bits.
+ */
+
+/* out[r] = scale * table[ids[r]].  table [vocab][hidden] (dtype), ids int32
+ * [rows], out [rows][hidden] (out_dtype; the residual stream of the decode path
+ * is fp32).  A negative id is padding: its row is zero.  An id >= vocab raises
+ * ORTHRUS_DEVERR_TOKEN and its row is zero. */
+orthrus_status_t orthrus_embed_rows(const void *table, int32_t dtype, int32_t vocab, int32_t hidden,
+                                    const int32_t *ids, int32_t rows, float scale, void *out, int32_t out_dtype,
+                                    uint32_t *dev_err, void *stream);
+
+/* Gradient of orthrus_embed_rows in the table: dtable[v] = scale * sum of
+ * dout[r] over the rows with ids[r] = v, by sorted tokens.  dout
+ * [rows][hidden] (dout_dtype), dtable [vocab][hidden] (dtable_dtype).
+ * accumulate 0: the whole of dtable is written, zeros for ids that do not
+ * occur; accumulate 1: the sums are added to dtable, other rows stay as they
+ * were.  Padding rows (negative ids) take no part, whatever they hold; ids >=
+ * vocab neither, and raise ORTHRUS_DEVERR_TOKEN. */
+orthrus_status_t orthrus_embed_grad_workspace(int32_t rows, int32_t hidden, int32_t vocab, size_t *bytes);
+orthrus_status_t orthrus_embed_grad(const void *dout, int32_t dout_dtype, const int32_t *ids, int32_t rows,
+                                    int32_t hidden, int32_t vocab, float scale, int32_t accumulate, void *dtable,
+                                    int32_t dtable_dtype, void *workspace, size_t ws_bytes, uint32_t *dev_err,
+                                    void *stream);
+
+/* y = x * gain / sqrt(mean(x^2) + eps) per row: x [rows][hidden] (x_dtype: fp32,
+ * the residual stream's, or dtype), gain [hidden] and y [rows][hidden] (dtype).
+ * x in bf16 with gain and y in fp32 returns ORTHRUS_ERR_UNSUPPORTED. */
+orthrus_status_t orthrus_rmsnorm(const void *x, int32_t x_dtype, const void *gain, int32_t dtype, int32_t rows,
+                                 int32_t hidden, float eps, void *y, void *stream);
+
+/* Gradient of orthrus_rmsnorm: dy [rows][hidden] (dtype) to dx [rows][hidden]
+ * (x_dtype) and dgain [hidden] (fp32, summed over the rows; overwritten). */
+orthrus_status_t orthrus_rmsnorm_grad_workspace(int32_t rows, int32_t hidden, size_t *bytes);
+orthrus_status_t orthrus_rmsnorm_grad(const void *x, int32_t x_dtype, const void *gain, const void *dy, int32_t dtype,
+                                      int32_t rows, int32_t hidden, float eps, void *dx, float *dgain,
+                                      void *workspace, size_t ws_bytes, void *stream);
+
+/* Cross entropy through the LM head: per row, with z = w h,
+ *     lse = log sum_v exp(z_v),   loss = lse - z[target],
+ * over the whole vocabulary; the logits never reach memory.  h [rows][hidden]
+ * and w [vocab][hidden] (dtype), targets int32 [rows], loss and lse fp32
+ * [rows].  A negative target is an ignored row (loss 0).  A target >= vocab
+ * is ignored as well and raises ORTHRUS_DEVERR_TOKEN; a non-finite lse of a
+ * row that is not ignored raises ORTHRUS_DEVERR_NONFINITE. */
+orthrus_status_t orthrus_ce_lm_head_workspace(int32_t rows, int32_t hidden, int32_t vocab, int32_t dtype,
+                                              size_t *bytes);
+orthrus_status_t orthrus_ce_lm_head(const void *h, const void *w, int32_t dtype, const int32_t *targets, int32_t rows,
+                                    int32_t hidden, int32_t vocab, float *loss, float *lse, void *workspace,
+                                    size_t ws_bytes, uint32_t *dev_err, void *stream);
+
+/* Gradient of orthrus_ce_lm_head, from its lse and the upstream gradient
+ * dloss (fp32 [rows]):
+ *     dz = dloss * (softmax(z) - onehot(target)),  dh = dz w,  dw = dz^T h,
+ * in pieces of the vocabulary whose logits are recomputed.  dh [rows][hidden]
+ * and dw [vocab][hidden] (dtype; dw may be NULL: a frozen head) are
+ * overwritten.  An ignored row, and a row whose dloss is 0, has a zero dh
+ * and takes no part in dw, whatever its h and lse hold.  On the bf16 path dz
+ * is rounded to bf16 before its two products (the operand type of the tensor
+ * cores). */
+orthrus_status_t orthrus_ce_lm_head_grad_workspace(int32_t rows, int32_t hidden, int32_t vocab, int32_t dtype,
+                                                   int32_t weight_grad, size_t *bytes);
+orthrus_status_t orthrus_ce_lm_head_grad(const void *h, const void *w, int32_t dtype, const int32_t *targets,
+                                         const float *lse, const float *dloss, int32_t rows, int32_t hidden,
+                                         int32_t vocab, void *dh, void *dw, void *workspace, size_t ws_bytes,
+                                         uint32_t *dev_err, void *stream);
+
+/* Gradient of orthrus_kl_lm_head's forward KL in the diffusion view's hidden
+ * rows (the AR view and the head are frozen), from both log-sum-exps and the
+ * upstream gradient dkl (fp32 [rows]):
+ *     dz = dkl * (softmax(w h_diff) - softmax(w h_ar)),  dh_diff = dz w.
+ * h_ar, h_diff, dh_diff [rows][hidden] and w [vocab][hidden] (dtype), lse_ar
+ * and lse_diff fp32 [rows].  A row whose dkl is 0 has a zero dh_diff,
+ * whatever its hidden rows hold.  Rounding of dz as above. */
+orthrus_status_t orthrus_kl_lm_head_grad_workspace(int32_t rows, int32_t hidden, int32_t vocab, int32_t dtype,
+                                                   size_t *bytes);
+orthrus_status_t orthrus_kl_lm_head_grad(const void *h_ar, const void *h_diff, const void *w, int32_t dtype,
+                                         const float *lse_ar, const float *lse_diff, const float *dkl, int32_t rows,
+                                         int32_t hidden, int32_t vocab, void *dh_diff, void *workspace,
+                                         size_t ws_bytes, uint32_t *dev_err, void *stream);
 
 /*
  * Test and measurement hook: the logits of the last verify (which = 0) or
