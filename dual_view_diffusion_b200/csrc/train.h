@@ -85,6 +85,17 @@ struct LossArgs {
 
 size_t loss_fwd_workspace(int N, int d, int V, int dtype);
 size_t loss_grad_workspace(int N, int d, int V, int dtype, int want_dw, int kl);
+// the tensor-core path (vocab_loss_tc.cu): bf16, hidden a multiple of 8,
+// 16-byte aligned buffers
+bool loss_tc_ok(const LossArgs &a);
+size_t loss_fwd_workspace_tc(int N, int d, int V);
+size_t loss_grad_workspace_tc(int N, int d, int V, int want_dw, int kl);
+cudaError_t loss_fwd_tc(const LossArgs &a, cudaStream_t s);
+cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s);
+// shared kernels (vocab_loss.cu)
+cudaError_t launch_ce_finalize(const float2 *rec, const float *zt, const LossArgs &a, int n_tiles, cudaStream_t s);
+cudaError_t launch_part_sum(const float *part, int splits, size_t n, void *out, int dtype, cudaStream_t s);
+cudaError_t launch_clean_rows(const LossArgs &a, void *out, cudaStream_t s);
 cudaError_t launch_loss_fwd(const LossArgs &a, cudaStream_t s);
 cudaError_t launch_loss_grad(const LossArgs &a, cudaStream_t s);
 

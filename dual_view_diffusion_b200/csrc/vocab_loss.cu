@@ -173,6 +173,12 @@ __global__ void __launch_bounds__(256) ce_finalize_kernel(const float2 *rec, con
     loss[row] = L - zt[row];
 }
 
+cudaError_t launch_ce_finalize(const float2 *rec, const float *zt, const LossArgs &a, int n_tiles, cudaStream_t s)
+{
+    return launch_k(ce_finalize_kernel, (a.N + 31) / 32, 256, 0, s, rec, zt, a.targets, n_tiles, a.N, a.V, a.loss, a.lse,
+                    a.err);
+}
+
 // dz of one piece [v0, v0 + Vp) of the vocabulary, fp32.  A row whose
 // upstream gradient is zero, or that has no target, gets exact zeros
 // whatever its hidden row holds.
@@ -341,17 +347,19 @@ static SimtPlan plan_simt(int N, int d, int V, int es, int want_dw)
     return p;
 }
 
+// Room for either path: which one a bf16 call takes depends on its pointers.
 size_t loss_fwd_workspace(int N, int d, int V, int dtype)
 {
     WsPlan w;
     w.take((size_t)((V + kSt - 1) / kSt) * N * sizeof(float2));
     w.take((size_t)N * 4);
-    return w.total;
+    return dtype == ORTHRUS_BF16 && d % 8 == 0 ? std::max(w.total, loss_fwd_workspace_tc(N, d, V)) : w.total;
 }
 
 size_t loss_grad_workspace(int N, int d, int V, int dtype, int want_dw, int kl)
 {
-    return plan_simt(N, d, V, dtype == ORTHRUS_BF16 ? 2 : 4, want_dw).total;
+    const size_t simt = plan_simt(N, d, V, dtype == ORTHRUS_BF16 ? 2 : 4, want_dw).total;
+    return dtype == ORTHRUS_BF16 && d % 8 == 0 ? std::max(simt, loss_grad_workspace_tc(N, d, V, want_dw, kl)) : simt;
 }
 
 // ---------------------------------------------------------------- launches
@@ -364,8 +372,7 @@ template <class T> static cudaError_t loss_fwd_simt(const LossArgs &a, cudaStrea
     cudaError_t e = launch_k(ce_tile_simt<T>, dim3(nt, (a.N + kSt - 1) / kSt), kStThreads, 0, s, (const T *)a.h,
                              (const T *)a.w, a.targets, a.N, a.d, a.V, rec, zt);
     if (e != cudaSuccess) return e;
-    return launch_k(ce_finalize_kernel, (a.N + 31) / 32, 256, 0, s, (const float2 *)rec, (const float *)zt, a.targets, nt,
-                    a.N, a.V, a.loss, a.lse, a.err);
+    return launch_ce_finalize(rec, zt, a, nt, s);
 }
 
 template <class T> static cudaError_t loss_grad_simt(const LossArgs &a, cudaStream_t s)
@@ -402,6 +409,7 @@ template <class T> static cudaError_t loss_grad_simt(const LossArgs &a, cudaStre
 cudaError_t launch_loss_fwd(const LossArgs &a, cudaStream_t s)
 {
     if (a.N == 0) return cudaSuccess;
+    if (loss_tc_ok(a)) return loss_fwd_tc(a, s);
     return a.dtype == ORTHRUS_BF16 ? loss_fwd_simt<bf16>(a, s) : loss_fwd_simt<float>(a, s);
 }
 
@@ -412,6 +420,7 @@ cudaError_t launch_loss_grad(const LossArgs &a, cudaStream_t s)
         return launch_k(zero_kernel, 2 * 148, 1024, 0, s, a.dw,
                         (size_t)a.V * a.d * (a.dtype == ORTHRUS_BF16 ? 2 : 4));
     }
+    if (loss_tc_ok(a)) return loss_grad_tc(a, s);
     return a.dtype == ORTHRUS_BF16 ? loss_grad_simt<bf16>(a, s) : loss_grad_simt<float>(a, s);
 }
 

@@ -1,0 +1,711 @@
+// The vocabulary losses on the 5th-generation tensor cores (bf16, rows of a
+// multiple of 8 elements, 16-byte aligned buffers).
+//
+// One persistent kernel runs every product of the losses as tiles of 256 x bn
+// per pair of SMs (tcgen05.mma.cta_group::2: each CTA of a 2-CTA cluster
+// holds 128 rows of A and bn/2 rows of B in shared memory and 128 accumulator
+// rows in its TMEM, so a k step reads half the shared memory of two separate
+// 128-row tiles, which is what held those back).  What differs between the
+// products is the operands' order in memory and the epilogue:
+//
+//   LSE   z = h W^T          epilogue: (max, sum exp) per (row, tile), target logit
+//   DZ    z = h W^T          epilogue: dz = g (exp(z - lse) - [v = t]), bf16
+//   DZKL  z of interleaved (AR, diffusion) rows: dz = g (p_diff - p_AR), bf16
+//   DH    dh += dz W         A = dz rows, B = W read along its rows (MN-major)
+//   DW    dW  = dz^T h       both operands MN-major
+//
+//   warp 0      producer: one thread issues the CTA's TMA loads into a ring of
+//               shared-memory stages; both CTAs' loads count on the first
+//               CTA's mbarrier
+//   warp 1      MMA issuer (first CTA of the pair only)
+//   warps 4..7  epilogue: one accumulator row per thread, 32 columns at a time
+//
+// Two accumulators (2 x 256 TMEM columns) let the next tile's MMAs run under
+// an epilogue.  Every wait is bounded: on timeout the kernel raises
+// ORTHRUS_DEVERR_TIMEOUT, stops issuing, lets its copies land and still frees
+// its TMEM.
+#include <cuda.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "train.h"
+
+namespace orthrus {
+
+bool make_tmap_box(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows);
+
+constexpr int kVlThreads = 256;
+constexpr int kVlEpi = 128;                    // epilogue threads per CTA
+constexpr int kVlM = 256;                      // rows of a pair's tile
+constexpr int kVlNMax = 256;                   // columns of a pair's tile
+constexpr int kVlK = 64;                       // k per stage
+constexpr uint32_t kVlABytes = 128 * kVlK * 2; // A bytes of a CTA's stage
+constexpr int kVlStages = 7;
+constexpr int kVlPairs = 74;                   // 2-CTA clusters that fit at once on 148 SMs
+constexpr int kVlJobs = 3;
+constexpr long long kVlSpinCycles = 4000000000LL;   // ~2 s at the B200 SM clock
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum VlKind : int { VL_LSE = 0, VL_DZ = 1, VL_DZKL = 2, VL_DH = 3, VL_DW = 4 };
+
+// One product of a launch: mt x nt x splits tiles.
+struct VlJob {
+    CUtensorMap a, b;
+    int kind;
+    int M, N;            // valid rows and columns of the result
+    int chunks, splits;  // 64-wide k chunks, and the shares they are cut into (DH)
+    int bn, mt, nt;
+    int b_off;           // B's first row (K-major) or first k row (MN-major): the piece's offset in W
+    int n_fast;          // tile order: 1 = columns first, 0 = rows first
+    // epilogue
+    const int32_t *targets;
+    const float *lse, *lse2, *g;
+    float2 *rec;         // LSE: [nt][M]
+    float *zt;           // LSE: [M]
+    bf16 *dz;            // DZ: [rows][pitch]
+    int v0, V, pitch;    // DZ: the piece's first id, the vocabulary, dz's row length
+    float *part;         // DH: [splits][M][N] fp32
+    int add, last;       // DH: add to part; the last piece of an unsplit dh: write out
+    bf16 *out;           // DH: [M][N]; DW: [M][N]
+};
+struct VlParams {
+    VlJob job[kVlJobs];
+    int jobs, pairs;
+    unsigned *err;
+    // job 0: tiles p, p + pairs, ..; job j > 0: tiles [first[j][p], first[j][p + 1])
+    uint16_t first[kVlJobs][kVlPairs + 1];
+};
+
+// ---------------------------------------------------------------- PTX wrappers
+__device__ __forceinline__ void vl_mbar_init(uint64_t *b, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(smem_u32(b)), "r"(count));
+}
+__device__ __forceinline__ void vl_expect_tx(uint64_t *b, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+// arrive on the barrier at shared::cluster address a (this CTA's or the peer's)
+__device__ __forceinline__ void vl_arrive_at(uint32_t a)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(a) : "memory");
+}
+__device__ __forceinline__ bool vl_try(uint64_t *b, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+                 " selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
+    return ok != 0;
+}
+// Bounded wait (about two seconds of SM clock); false on timeout, or when
+// another role of the CTA already gave up.
+__device__ __forceinline__ bool vl_wait(uint64_t *b, uint32_t parity, volatile int *abort)
+{
+    if (vl_try(b, parity)) return true;
+    const long long t0 = clock64();
+    for (long i = 0;; ++i) {
+        if (vl_try(b, parity)) return true;
+        if ((i & 255) == 255) {
+            if (*abort) return false;
+            if (clock64() - t0 > kVlSpinCycles) break;
+        }
+    }
+    *abort = 1;
+    return false;
+}
+__device__ __forceinline__ uint32_t vl_mapa(uint32_t local, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+// TMA tile load whose bytes count on a barrier of either CTA of the pair.
+__device__ __forceinline__ void vl_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n"
+        ::"r"(dst), "l"((uint64_t)map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+// Shared-memory descriptors, 128-byte swizzle (layout code 2, version 1).
+// K-major: rows of 64 k, 8-row groups 1024 B apart; a k step of 16 is 32 B.
+__device__ __forceinline__ uint64_t vl_desc_k(uint32_t a)
+{
+    return (uint64_t)((a & 0x3FFFF) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+           ((uint64_t)2 << 61);
+}
+// MN-major: k rows of 64 elements along M or N; 8-k groups 1024 B apart, the
+// next 64 elements along M or N 8192 B on (one TMA box); a k step of 16 is
+// 2048 B.
+__device__ __forceinline__ uint64_t vl_desc_mn(uint32_t a)
+{
+    return (uint64_t)((a & 0x3FFFF) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ void vl_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// arrive on this barrier of both CTAs once the MMAs issued so far are done
+__device__ __forceinline__ void vl_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n"
+                 ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+                 : "memory");
+}
+__device__ __forceinline__ void vl_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void vl_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void vl_cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void vl_tmem_ld32(uint32_t taddr, float (&r)[32])
+{
+    uint32_t u[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+          "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
+          "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
+          "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = __uint_as_float(u[i]);
+}
+__device__ __forceinline__ float vl_exp2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *(const uint32_t *)&h;
+}
+
+// ---------------------------------------------------------------- tiles
+struct VlTile {
+    int m0, n0, nt, split, c0, c1;   // first row and column, column tile, k chunks [c0, c1)
+};
+// The tiles of pair p, in order, over all jobs of the launch.
+struct VlIter {
+    const VlParams &prm;
+    int p, j, t, end, step;
+    __device__ VlIter(const VlParams &prm_, int p_) : prm(prm_), p(p_), j(-1), t(0), end(0), step(1) { next_job(); }
+    __device__ void next_job()
+    {
+        while (++j < prm.jobs) {
+            const VlJob &jb = prm.job[j];
+            if (j == 0) { t = p; step = prm.pairs; end = jb.mt * jb.nt * jb.splits; }
+            else { t = prm.first[j][p]; step = 1; end = prm.first[j][p + 1]; }
+            if (t < end) return;
+        }
+    }
+    __device__ bool valid() const { return j < prm.jobs; }
+    __device__ VlTile get() const
+    {
+        const VlJob &jb = prm.job[j];
+        VlTile x;
+        int r = t, m, n;
+        if (jb.n_fast) { n = r % jb.nt; r /= jb.nt; m = r % jb.mt; r /= jb.mt; }
+        else { m = r % jb.mt; r /= jb.mt; n = r % jb.nt; r /= jb.nt; }
+        x.m0 = m * kVlM;
+        x.n0 = n * jb.bn;
+        x.nt = n;
+        x.split = r;
+        x.c0 = (int)((long)jb.chunks * r / jb.splits);
+        x.c1 = (int)((long)jb.chunks * (r + 1) / jb.splits);
+        return x;
+    }
+    __device__ void advance()
+    {
+        t += step;
+        if (t >= end) next_job();
+    }
+};
+
+struct VlSmem {
+    alignas(8) uint64_t full[kVlStages], empty[kVlStages], tfull[2], tempty[2];
+    uint32_t tmem_base;
+    int abort;
+};
+
+// ---------------------------------------------------------------- epilogues
+// taddr: the accumulator's first column, this warp's lanes.
+__device__ __forceinline__ void vl_epi_lse(const VlJob &jb, const VlTile &x, int row, uint32_t taddr)
+{
+    const int nv = min(jb.bn, jb.N - x.n0);           // ids of this tile below the vocabulary
+    const int id = row < jb.M ? jb.targets[row] : -1, t = id < 0 ? -1 : id - x.n0;
+    float m = -INFINITY, s = 0.f, z_t = 0.f;
+    for (int c = 0; c < nv; c += 32) {
+        float r[32];
+        vl_tmem_ld32(taddr + c, r);
+        if (nv - c < 32)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (c + i >= nv) r[i] = -INFINITY;
+        if (t >= c && t < c + 32)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (t == c + i) z_t = r[i];
+        float cm = r[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) cm = fmaxf(cm, r[i]);
+        const float mn = fmaxf(m, cm), k = (mn == -INFINITY ? 0.f : mn) * kLog2e;   // (a NaN logit makes the sum NaN)
+        float a[4] = {s * vl_exp2(fmaf(m, kLog2e, -k)), 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) a[i & 3] += vl_exp2(fmaf(r[i], kLog2e, -k));
+        s = (a[0] + a[1]) + (a[2] + a[3]);
+        m = mn;
+    }
+    if (row < jb.M) {
+        jb.rec[(size_t)x.nt * jb.M + row] = make_float2(m, s);
+        if (t >= 0 && t < nv) jb.zt[row] = z_t;
+    }
+}
+
+// 16 bf16 columns of a row of dz
+__device__ __forceinline__ void vl_store16(bf16 *p, const float (&v)[16])
+{
+    ((uint4 *)p)[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    ((uint4 *)p)[1] = make_uint4(pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]), pack_bf16(v[12], v[13]), pack_bf16(v[14], v[15]));
+}
+
+__device__ __forceinline__ void vl_epi_dz(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, unsigned *err)
+{
+    float g = 0.f, k = 0.f;
+    int t = -1;
+    if (row < jb.M) {
+        const int id = jb.targets[row];
+        if (id >= jb.V && x.n0 == 0 && jb.v0 == 0 && err) raise_err(err, ORTHRUS_DEVERR_TOKEN);
+        if (id >= 0 && id < jb.V) { g = jb.g[row]; t = id - jb.v0 - x.n0; }
+        k = jb.lse[row] * kLog2e;
+    }
+    const int nv = jb.N - x.n0;                        // columns of the tile below the piece's end (may exceed bn)
+    const int nc = min(jb.bn, jb.pitch - x.n0);        // columns dz has room for
+    bf16 *dst = jb.dz + (size_t)row * jb.pitch + x.n0;
+    for (int c = 0; c < nc; c += 32) {
+        float r[32];
+        vl_tmem_ld32(taddr + c, r);
+        if (row >= jb.M) continue;
+#pragma unroll
+        for (int h = 0; h < 32; h += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float e = vl_exp2(fmaf(r[h + i], kLog2e, -k));
+                if (c + h + i == t) e -= 1.f;
+                // rows without a share and columns past the vocabulary are exact zeros
+                v[i] = g == 0.f || c + h + i >= nv ? 0.f : g * e;
+            }
+            vl_store16(dst + c + h, v);
+        }
+    }
+}
+
+// Interleaved rows: even lanes hold the AR view's logits of a position, odd
+// lanes the diffusion view's.  Each pair of lanes exchanges halves of a chunk
+// and writes 16 columns per lane.
+__device__ __forceinline__ void vl_epi_dzkl(const VlJob &jb, const VlTile &x, int row, uint32_t taddr)
+{
+    const int pos = row >> 1, odd = row & 1;
+    const bool live = row < jb.M;
+    const float k = live ? (odd ? jb.lse2 : jb.lse)[pos] * kLog2e : 0.f, g = live ? jb.g[pos] : 0.f;
+    const int nv = jb.N - x.n0;
+    const int nc = min(jb.bn, jb.pitch - x.n0);
+    bf16 *dst = jb.dz + (size_t)pos * jb.pitch + x.n0 + 16 * odd;
+    for (int c = 0; c < nc; c += 32) {
+        float r[32], v[16];
+        vl_tmem_ld32(taddr + c, r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = vl_exp2(fmaf(r[i], kLog2e, -k));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float mine = odd ? r[16 + i] : r[i];
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? r[i] : r[16 + i], 1);
+            const float e = odd ? mine - other : other - mine;   // p_diff - p_AR
+            v[i] = g == 0.f || c + 16 * odd + i >= nv ? 0.f : g * e;
+        }
+        if (live) vl_store16(dst + c, v);
+    }
+}
+
+// dh: this piece's share, added to what earlier pieces left
+__device__ __forceinline__ void vl_epi_dh(const VlJob &jb, const VlTile &x, int row, uint32_t taddr)
+{
+    const int nv = min(jb.bn, jb.N - x.n0);            // (a multiple of 8)
+    const bool out = jb.last;
+    float *p = jb.part + ((size_t)x.split * jb.M + row) * jb.N + x.n0;
+    bf16 *o = jb.out + (size_t)row * jb.N + x.n0;
+    for (int c = 0; c < nv; c += 32) {
+        float r[32];
+        vl_tmem_ld32(taddr + c, r);
+        if (row >= jb.M) continue;
+#pragma unroll
+        for (int q = 0; q < 32; q += 8) {
+            if (c + q >= nv) break;
+            float4 *f = (float4 *)(p + c + q);
+            float4 a = make_float4(r[q], r[q + 1], r[q + 2], r[q + 3]), b = make_float4(r[q + 4], r[q + 5], r[q + 6], r[q + 7]);
+            if (jb.add) {
+                const float4 u = f[0], w = f[1];
+                a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+                b.x += w.x; b.y += w.y; b.z += w.z; b.w += w.w;
+            }
+            if (out)
+                *(uint4 *)(o + c + q) = make_uint4(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w), pack_bf16(b.x, b.y), pack_bf16(b.z, b.w));
+            else { f[0] = a; f[1] = b; }
+        }
+    }
+}
+
+__device__ __forceinline__ void vl_epi_dw(const VlJob &jb, const VlTile &x, int row, uint32_t taddr)
+{
+    const int nv = min(jb.bn, jb.N - x.n0);
+    bf16 *o = jb.out + (size_t)row * jb.N + x.n0;
+    for (int c = 0; c < nv; c += 32) {
+        float r[32];
+        vl_tmem_ld32(taddr + c, r);
+        if (row >= jb.M) continue;
+#pragma unroll
+        for (int q = 0; q < 32; q += 8) {
+            if (c + q >= nv) break;
+            *(uint4 *)(o + c + q) = make_uint4(pack_bf16(r[q], r[q + 1]), pack_bf16(r[q + 2], r[q + 3]),
+                                               pack_bf16(r[q + 4], r[q + 5]), pack_bf16(r[q + 6], r[q + 7]));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- kernel
+__global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_constant__ VlParams prm)
+{
+    extern __shared__ __align__(1024) unsigned char vl_smem_raw[];
+    __shared__ VlSmem sm;
+    const uint32_t ring = (smem_u32(vl_smem_raw) + 1023) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = blockIdx.x & 1;               // CTA of the pair
+    const int pair = blockIdx.x >> 1;
+    volatile int *abort = &sm.abort;
+    constexpr uint32_t kStage = kVlABytes + kVlNMax / 2 * kVlK * 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kVlStages; ++s) { vl_mbar_init(&sm.full[s], 1); vl_mbar_init(&sm.empty[s], 1); }
+        for (int s = 0; s < 2; ++s) { vl_mbar_init(&sm.tfull[s], 1); vl_mbar_init(&sm.tempty[s], 2 * kVlEpi / 32); }
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sm.tmem_base)),
+                     "r"(512u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
+    }
+    vl_fence_before();
+    __syncthreads();
+    vl_cluster_sync();                                  // both CTAs' barriers and TMEM are ready
+    vl_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    pdl_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {   // ------------------------------------------- producer
+            uint32_t stage = 0, phase = 0;
+            bool stop = false;
+            for (VlIter it(prm, pair); it.valid() && !stop; it.advance()) {
+                const VlJob &jb = prm.job[it.j];
+                const VlTile x = it.get();
+                const int am = x.m0 + (int)rank * 128, bnh = jb.bn / 2, bx = x.n0 + (int)rank * bnh;
+                const uint32_t bytes = 2 * (kVlABytes + (uint32_t)bnh * kVlK * 2);
+                for (int c = x.c0; c < x.c1; ++c) {
+                    if (!vl_wait(&sm.empty[stage], phase ^ 1, abort) || *abort) { stop = true; break; }
+                    if (rank == 0) vl_expect_tx(&sm.full[stage], bytes);
+                    const uint32_t bar = vl_mapa(smem_u32(&sm.full[stage]), 0);
+                    const uint32_t a = ring + stage * kStage, b = a + kVlABytes;
+                    const int k = c * kVlK;
+                    if (jb.kind == VL_DW) {
+                        vl_load(a, &jb.a, am, k, bar);
+                        vl_load(a + 8192, &jb.a, am + 64, k, bar);
+                    } else {
+                        vl_load(a, &jb.a, k, am, bar);
+                    }
+                    if (jb.kind >= VL_DH) {
+                        for (int q = 0; q < bnh; q += 64) vl_load(b + q * 128, &jb.b, bx + q, jb.b_off + k, bar);
+                    } else {
+                        vl_load(b, &jb.b, k, jb.b_off + bx, bar);
+                    }
+                    if (++stage == (uint32_t)kVlStages) { stage = 0; phase ^= 1; }
+                }
+            }
+            pdl_trigger();
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {   // ------------------------------ MMA issuer
+            uint32_t stage = 0, phase = 0;
+            int local = 0;
+            for (VlIter it(prm, pair); it.valid() && !*abort; it.advance(), ++local) {
+                const VlJob &jb = prm.job[it.j];
+                const VlTile x = it.get();
+                const int acc = local & 1;
+                const bool a_mn = jb.kind == VL_DW, b_mn = jb.kind >= VL_DH;
+                const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
+                                       ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(jb.bn >> 3) << 17) |
+                                       ((uint32_t)(kVlM >> 4) << 24);
+                const uint64_t as = a_mn ? 2048 >> 4 : 32 >> 4, bs = b_mn ? 2048 >> 4 : 32 >> 4;
+                if (!vl_wait(&sm.tempty[acc], ((local >> 1) & 1) ^ 1, abort)) break;
+                vl_fence_after();
+                const uint32_t d = tmem + acc * kVlNMax;
+                bool ok = true;
+                for (int c = x.c0; c < x.c1; ++c) {
+                    if (!vl_wait(&sm.full[stage], phase, abort)) { ok = false; break; }
+                    vl_fence_after();
+                    const uint32_t a = ring + stage * kStage, b = a + kVlABytes;
+                    const uint64_t ad = a_mn ? vl_desc_mn(a) : vl_desc_k(a), bd = b_mn ? vl_desc_mn(b) : vl_desc_k(b);
+#pragma unroll
+                    for (int k = 0; k < kVlK / 16; ++k)
+                        vl_mma(d, ad + as * k, bd + bs * k, idesc, (c > x.c0 || k > 0) ? 1u : 0u);
+                    vl_commit(&sm.empty[stage]);
+                    if (++stage == (uint32_t)kVlStages) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+                vl_commit(&sm.tfull[acc]);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {   // ---------------------------------------- epilogue
+        const int q = warp & 3;                          // TMEM lane quarter of this warp
+        const int r = (int)rank * 128 + q * 32 + lane;   // row in the tile
+        const uint32_t free0 = vl_mapa(smem_u32(&sm.tempty[0]), 0), free1 = vl_mapa(smem_u32(&sm.tempty[1]), 0);
+        int local = 0;
+        for (VlIter it(prm, pair); it.valid(); it.advance(), ++local) {
+            const VlJob &jb = prm.job[it.j];
+            const VlTile x = it.get();
+            const int acc = local & 1, row = x.m0 + r;
+            const bool ok = vl_wait(&sm.tfull[acc], (local >> 1) & 1, abort);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            vl_fence_after();
+            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kVlNMax;
+            if (x.m0 + (int)rank * 128 + q * 32 < jb.M) {   // (whole warps past the last row have nothing to do)
+                switch (jb.kind) {
+                case VL_LSE: vl_epi_lse(jb, x, row, taddr); break;
+                case VL_DZ: vl_epi_dz(jb, x, row, taddr, prm.err); break;
+                case VL_DZKL: vl_epi_dzkl(jb, x, row, taddr); break;
+                case VL_DH: vl_epi_dh(jb, x, row, taddr); break;
+                default: vl_epi_dw(jb, x, row, taddr); break;
+                }
+            }
+            vl_fence_before();
+            __syncwarp();
+            if (lane == 0) vl_arrive_at(acc ? free1 : free0);
+        }
+    }
+
+    vl_fence_before();
+    __syncthreads();
+    if (*abort) {   // let this CTA's copies and MMAs in flight land before the memory goes away
+        const long long t0 = clock64();
+        while (clock64() - t0 < 20000000LL) {}
+        if (threadIdx.x == 0 && prm.err) raise_err(prm.err, ORTHRUS_DEVERR_TIMEOUT);
+    }
+    vl_cluster_sync();                                  // the peer may still signal this CTA's barriers
+    if (warp == 2) {
+        vl_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+    }
+}
+
+// rows 2i and 2i + 1 of out: row i of the AR and of the diffusion view; with a
+// zero upstream gradient both are zero (so their values cannot matter)
+__global__ void __launch_bounds__(256) vl_interleave_kernel(const uint4 *ra, const uint4 *rb, const float *g, uint4 *out,
+                                                            int vecs)
+{
+    pdl_trigger();
+    pdl_wait();
+    const int r = blockIdx.x;
+    const bool live = g[r] != 0.f;
+    const uint4 z = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < vecs; i += 256) {
+        out[(size_t)(2 * r) * vecs + i] = live ? ra[(size_t)r * vecs + i] : z;
+        out[(size_t)(2 * r + 1) * vecs + i] = live ? rb[(size_t)r * vecs + i] : z;
+    }
+}
+
+// ---------------------------------------------------------------- host
+static size_t up(size_t x, size_t m) { return (x + m - 1) / m * m; }
+
+// Columns per tile of z: 256, unless a single row tile leaves so few tiles
+// that whole rounds of the pairs waste more than narrower tiles do.
+static int vl_bn(int rows, long cols)
+{
+    if (rows > kVlM) return kVlNMax;
+    int best = kVlNMax;
+    long cost = -1;
+    for (int bn = kVlNMax; bn >= 128; bn -= 64) {
+        const long t = ((cols + bn - 1) / bn + kVlPairs - 1) / kVlPairs * (bn + 8);
+        if (cost < 0 || t < cost) { cost = t; best = bn; }
+    }
+    return best;
+}
+
+// Shares of dh's k axis: the smallest count that keeps the rounds of the
+// pairs nearly full, each share at least 8 chunks.
+static int vl_splits(long tiles, long chunks)
+{
+    int best = 1;
+    double cost = 1e30;
+    for (int s = 1; s <= 32 && (s == 1 || chunks / s >= 8); ++s) {
+        const double t = (double)((tiles * s + kVlPairs - 1) / kVlPairs) / s * (1.0 + 0.02 * s);
+        if (t < cost) { cost = t; best = s; }
+    }
+    return best;
+}
+
+bool loss_tc_ok(const LossArgs &a)
+{
+    auto al = [](const void *p) { return ((uintptr_t)p & 15) == 0; };
+    return a.dtype == ORTHRUS_BF16 && a.d % 8 == 0 && al(a.h) && al(a.h2) && al(a.w) && al(a.dh) && al(a.dw);
+}
+
+static cudaError_t vl_launch(VlParams &p, cudaStream_t s)
+{
+    long tiles = 0;
+    for (int j = 0; j < p.jobs; ++j) tiles += (long)p.job[j].mt * p.job[j].nt * p.job[j].splits;
+    p.pairs = (int)std::min<long>(kVlPairs, tiles);
+    const size_t smem = 1024 + (size_t)kVlStages * (kVlABytes + kVlNMax / 2 * kVlK * 2);
+    cudaError_t e = cudaFuncSetAttribute(vocab_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * p.pairs);
+    cfg.blockDim = dim3(kVlThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, vocab_pair_kernel, p);
+}
+
+size_t loss_fwd_workspace_tc(int N, int d, int V)
+{
+    WsPlan w;
+    w.take((size_t)((V + 127) / 128) * N * sizeof(float2));
+    w.take((size_t)N * 4);
+    return w.total;
+}
+
+cudaError_t loss_fwd_tc(const LossArgs &a, cudaStream_t s)
+{
+    WsPlan w;
+    float2 *rec = (float2 *)(a.ws + w.take((size_t)((a.V + 127) / 128) * a.N * sizeof(float2)));
+    float *zt = (float *)(a.ws + w.take((size_t)a.N * 4));
+    VlParams p;
+    memset(&p, 0, sizeof(p));
+    VlJob &j = p.job[0];
+    j.kind = VL_LSE; j.M = a.N; j.N = a.V; j.chunks = (a.d + kVlK - 1) / kVlK; j.splits = 1;
+    j.bn = vl_bn(a.N, a.V); j.mt = (a.N + kVlM - 1) / kVlM; j.nt = (a.V + j.bn - 1) / j.bn;
+    j.targets = a.targets; j.rec = rec; j.zt = zt;
+    if (!make_tmap_box(&j.a, a.h, a.N, a.d, kVlK, 128) || !make_tmap_box(&j.b, a.w, a.V, a.d, kVlK, j.bn / 2))
+        return cudaErrorInvalidValue;
+    p.jobs = 1; p.err = a.err;
+    cudaError_t e = vl_launch(p, s);
+    if (e != cudaSuccess) return e;
+    return launch_ce_finalize(rec, zt, a, j.nt, s);
+}
+
+struct VlPlan {
+    size_t total, o_dz, o_part, o_h;
+    int piece, splits, bn, zrows;
+};
+static VlPlan vl_plan(int N, int d, int V, int want_dw, int kl)
+{
+    VlPlan p{};
+    WsPlan w;
+    // a piece's dz stays within 128 MiB: large enough that a piece's products
+    // fill many rounds of the pairs, and bounded whatever the vocabulary
+    const size_t cap = std::max<size_t>(256, ((size_t)128 << 20) / (2 * (size_t)N) / 256 * 256);
+    p.piece = (int)std::min(cap, up(V, 256));
+    p.zrows = kl ? 2 * N : N;
+    p.bn = vl_bn(p.zrows, std::min(p.piece, V));
+    const long tiles = (long)up(N, kVlM) / kVlM * ((d + 255) / 256);
+    p.splits = vl_splits(tiles, (std::min(p.piece, V) + kVlK - 1) / kVlK);
+    p.o_dz = w.take((size_t)N * p.piece * 2);
+    p.o_part = w.take((size_t)p.splits * N * d * 4);
+    p.o_h = w.take(kl ? (size_t)2 * N * d * 2 : want_dw ? (size_t)N * d * 2 : 0);
+    p.total = w.total;
+    return p;
+}
+
+size_t loss_grad_workspace_tc(int N, int d, int V, int want_dw, int kl) { return vl_plan(N, d, V, want_dw, kl).total; }
+
+cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
+{
+    const int N = a.N, d = a.d;
+    const VlPlan pl = vl_plan(N, d, a.V, a.dw != nullptr, a.kl);
+    bf16 *dz = (bf16 *)(a.ws + pl.o_dz), *hx = (bf16 *)(a.ws + pl.o_h);
+    float *part = (float *)(a.ws + pl.o_part);
+    cudaError_t e = cudaSuccess;
+    if (a.kl)
+        e = launch_k(vl_interleave_kernel, N, 256, 0, s, (const uint4 *)a.h, (const uint4 *)a.h2, a.g, (uint4 *)hx, d / 8);
+    else if (a.dw)
+        e = launch_clean_rows(a, hx, s);
+    if (e != cudaSuccess) return e;
+    CUtensorMap zh, zw, dzk, dzm, wm, hm;
+    const bool ok = make_tmap_box(&zh, a.kl ? (const void *)hx : a.h, pl.zrows, d, kVlK, 128) &&
+                    make_tmap_box(&zw, a.w, a.V, d, kVlK, pl.bn / 2) &&
+                    make_tmap_box(&dzk, dz, N, pl.piece, kVlK, 128) && make_tmap_box(&dzm, dz, N, pl.piece, 64, kVlK) &&
+                    make_tmap_box(&wm, a.w, a.V, d, 64, kVlK) && (!a.dw || make_tmap_box(&hm, hx, N, d, 64, kVlK));
+    if (!ok) return cudaErrorInvalidValue;
+    VlParams p;
+    for (int v0 = 0; v0 < a.V; v0 += pl.piece) {
+        const int nv = std::min(pl.piece, a.V - v0);
+        {
+            memset(&p, 0, sizeof(p));
+            VlJob &j = p.job[0];
+            j.kind = a.kl ? VL_DZKL : VL_DZ; j.M = pl.zrows; j.N = nv; j.chunks = (d + kVlK - 1) / kVlK; j.splits = 1;
+            j.bn = pl.bn; j.mt = (pl.zrows + kVlM - 1) / kVlM; j.nt = (nv + j.bn - 1) / j.bn;
+            j.b_off = v0; j.targets = a.targets; j.lse = a.lse_in; j.lse2 = a.lse2_in; j.g = a.g;
+            j.dz = dz; j.v0 = v0; j.V = a.V; j.pitch = pl.piece;
+            j.a = zh; j.b = zw;
+            p.jobs = 1; p.err = a.err;
+            if ((e = vl_launch(p, s)) != cudaSuccess) return e;
+        }
+        {
+            memset(&p, 0, sizeof(p));
+            VlJob &j = p.job[0];
+            j.kind = VL_DH; j.M = N; j.N = d; j.chunks = (nv + kVlK - 1) / kVlK;
+            j.splits = std::min(pl.splits, j.chunks);
+            j.bn = 256; j.mt = (N + kVlM - 1) / kVlM; j.nt = (d + 255) / 256;
+            j.b_off = v0; j.part = part; j.add = v0 > 0; j.last = pl.splits == 1 && v0 + pl.piece >= a.V; j.out = (bf16 *)a.dh;
+            j.a = dzk; j.b = wm;
+            p.jobs = 1; p.err = a.err;
+            if ((e = vl_launch(p, s)) != cudaSuccess) return e;
+        }
+        if (a.dw) {
+            memset(&p, 0, sizeof(p));
+            VlJob &j = p.job[0];
+            j.kind = VL_DW; j.M = nv; j.N = d; j.chunks = (N + kVlK - 1) / kVlK; j.splits = 1;
+            j.bn = 256; j.mt = (nv + kVlM - 1) / kVlM; j.nt = (d + 255) / 256; j.n_fast = 1;
+            j.out = (bf16 *)a.dw + (size_t)v0 * d;
+            j.a = dzm; j.b = hm;
+            p.jobs = 1; p.err = a.err;
+            if ((e = vl_launch(p, s)) != cudaSuccess) return e;
+        }
+    }
+    if (pl.splits > 1) return launch_part_sum(part, pl.splits, (size_t)N * d, a.dh, ORTHRUS_BF16, s);
+    return cudaSuccess;
+}
+
+}  // namespace orthrus
