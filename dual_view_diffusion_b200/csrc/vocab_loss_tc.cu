@@ -40,9 +40,9 @@ constexpr int kVlThreads = 256;
 constexpr int kVlEpi = 128;                    // epilogue threads per CTA
 constexpr int kVlM = 256;                      // rows of a pair's tile
 constexpr int kVlNMax = 256;                   // columns of a pair's tile
-constexpr int kVlK = 64;                       // k per stage
+constexpr int kVlK = 128;                      // k per stage: eight MMAs for each wait and commit
 constexpr uint32_t kVlABytes = 128 * kVlK * 2; // A bytes of a CTA's stage
-constexpr int kVlStages = 7;
+constexpr int kVlStages = 3;
 constexpr int kVlPairs = 74;                   // 2-CTA clusters that fit at once on 148 SMs
 constexpr int kVlJobs = 3;
 constexpr long long kVlSpinCycles = 4000000000LL;   // ~2 s at the B200 SM clock
@@ -55,7 +55,7 @@ struct VlJob {
     CUtensorMap a, b;
     int kind;
     int M, N;            // valid rows and columns of the result
-    int chunks, splits;  // 64-wide k chunks, and the shares they are cut into (DH)
+    int chunks, splits;  // k chunks of kVlK, and the shares they are cut into (DH)
     int bn, mt, nt;
     int b_off;           // B's first row (K-major) or first k row (MN-major): the piece's offset in W
     int n_fast;          // tile order: 1 = columns first, 0 = rows first
@@ -138,11 +138,11 @@ __device__ __forceinline__ uint64_t vl_desc_k(uint32_t a)
            ((uint64_t)2 << 61);
 }
 // MN-major: k rows of 64 elements along M or N; 8-k groups 1024 B apart, the
-// next 64 elements along M or N 8192 B on (one TMA box); a k step of 16 is
+// next 64 elements along M or N one TMA box (kVlK rows) on; a k step of 16 is
 // 2048 B.
 __device__ __forceinline__ uint64_t vl_desc_mn(uint32_t a)
 {
-    return (uint64_t)((a & 0x3FFFF) >> 4) | ((uint64_t)(8192 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+    return (uint64_t)((a & 0x3FFFF) >> 4) | ((uint64_t)(kVlK * 128 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 __device__ __forceinline__ void vl_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
@@ -429,16 +429,19 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
                     const uint32_t bar = vl_mapa(smem_u32(&sm.full[stage]), 0);
                     const uint32_t a = ring + stage * kStage, b = a + kVlABytes;
                     const int k = c * kVlK;
+                    // two boxes of 64 elements each: along k (K-major), or along M / N
                     if (jb.kind == VL_DW) {
                         vl_load(a, &jb.a, am, k, bar);
-                        vl_load(a + 8192, &jb.a, am + 64, k, bar);
+                        vl_load(a + kVlABytes / 2, &jb.a, am + 64, k, bar);
                     } else {
                         vl_load(a, &jb.a, k, am, bar);
+                        vl_load(a + kVlABytes / 2, &jb.a, k + 64, am, bar);
                     }
                     if (jb.kind >= VL_DH) {
-                        for (int q = 0; q < bnh; q += 64) vl_load(b + q * 128, &jb.b, bx + q, jb.b_off + k, bar);
+                        for (int q = 0; q < bnh; q += 64) vl_load(b + q * kVlK * 2, &jb.b, bx + q, jb.b_off + k, bar);
                     } else {
                         vl_load(b, &jb.b, k, jb.b_off + bx, bar);
+                        vl_load(b + bnh * 128, &jb.b, k + 64, jb.b_off + bx, bar);
                     }
                     if (++stage == (uint32_t)kVlStages) { stage = 0; phase ^= 1; }
                 }
@@ -458,7 +461,9 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
                 const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
                                        ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(jb.bn >> 3) << 17) |
                                        ((uint32_t)(kVlM >> 4) << 24);
+                // descriptor steps: 16 k inside a 64-k half of the stage, and the other half
                 const uint64_t as = a_mn ? 2048 >> 4 : 32 >> 4, bs = b_mn ? 2048 >> 4 : 32 >> 4;
+                const uint64_t ah = a_mn ? 4 * as : kVlABytes / 2 >> 4, bh = b_mn ? 4 * bs : (uint64_t)(jb.bn / 2 * 128 >> 4);
                 if (!vl_wait(&sm.tempty[acc], ((local >> 1) & 1) ^ 1, abort)) break;
                 vl_fence_after();
                 const uint32_t d = tmem + acc * kVlNMax;
@@ -470,7 +475,8 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
                     const uint64_t ad = a_mn ? vl_desc_mn(a) : vl_desc_k(a), bd = b_mn ? vl_desc_mn(b) : vl_desc_k(b);
 #pragma unroll
                     for (int k = 0; k < kVlK / 16; ++k)
-                        vl_mma(d, ad + as * k, bd + bs * k, idesc, (c > x.c0 || k > 0) ? 1u : 0u);
+                        vl_mma(d, ad + as * (k & 3) + ah * (k >> 2), bd + bs * (k & 3) + bh * (k >> 2), idesc,
+                               (c > x.c0 || k > 0) ? 1u : 0u);
                     vl_commit(&sm.empty[stage]);
                     if (++stage == (uint32_t)kVlStages) { stage = 0; phase ^= 1; }
                 }
@@ -547,7 +553,7 @@ static int vl_bn(int rows, long cols)
     if (rows > kVlM) return kVlNMax;
     int best = kVlNMax;
     long cost = -1;
-    for (int bn = kVlNMax; bn >= 128; bn -= 64) {
+    for (int bn = kVlNMax; bn >= 128; bn -= 128) {   // (a multiple of dh's k chunk)
         const long t = ((cols + bn - 1) / bn + kVlPairs - 1) / kVlPairs * (bn + 8);
         if (cost < 0 || t < cost) { cost = t; best = bn; }
     }
@@ -555,12 +561,12 @@ static int vl_bn(int rows, long cols)
 }
 
 // Shares of dh's k axis: the smallest count that keeps the rounds of the
-// pairs nearly full, each share at least 8 chunks.
+// pairs nearly full, each share at least 4 chunks.
 static int vl_splits(long tiles, long chunks)
 {
     int best = 1;
     double cost = 1e30;
-    for (int s = 1; s <= 32 && (s == 1 || chunks / s >= 8); ++s) {
+    for (int s = 1; s <= 32 && (s == 1 || chunks / s >= 4); ++s) {
         const double t = (double)((tiles * s + kVlPairs - 1) / kVlPairs) / s * (1.0 + 0.02 * s);
         if (t < cost) { cost = t; best = s; }
     }
@@ -617,7 +623,7 @@ cudaError_t loss_fwd_tc(const LossArgs &a, cudaStream_t s)
     j.kind = VL_LSE; j.M = a.N; j.N = a.V; j.chunks = (a.d + kVlK - 1) / kVlK; j.splits = 1;
     j.bn = vl_bn(a.N, a.V); j.mt = (a.N + kVlM - 1) / kVlM; j.nt = (a.V + j.bn - 1) / j.bn;
     j.targets = a.targets; j.rec = rec; j.zt = zt;
-    if (!make_tmap_box(&j.a, a.h, a.N, a.d, kVlK, 128) || !make_tmap_box(&j.b, a.w, a.V, a.d, kVlK, j.bn / 2))
+    if (!make_tmap_box(&j.a, a.h, a.N, a.d, 64, 128) || !make_tmap_box(&j.b, a.w, a.V, a.d, 64, j.bn / 2))
         return cudaErrorInvalidValue;
     p.jobs = 1; p.err = a.err;
     cudaError_t e = vl_launch(p, s);
@@ -663,9 +669,9 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
         e = launch_clean_rows(a, hx, s);
     if (e != cudaSuccess) return e;
     CUtensorMap zh, zw, dzk, dzm, wm, hm;
-    const bool ok = make_tmap_box(&zh, a.kl ? (const void *)hx : a.h, pl.zrows, d, kVlK, 128) &&
-                    make_tmap_box(&zw, a.w, a.V, d, kVlK, pl.bn / 2) &&
-                    make_tmap_box(&dzk, dz, N, pl.piece, kVlK, 128) && make_tmap_box(&dzm, dz, N, pl.piece, 64, kVlK) &&
+    const bool ok = make_tmap_box(&zh, a.kl ? (const void *)hx : a.h, pl.zrows, d, 64, 128) &&
+                    make_tmap_box(&zw, a.w, a.V, d, 64, pl.bn / 2) &&
+                    make_tmap_box(&dzk, dz, N, pl.piece, 64, 128) && make_tmap_box(&dzm, dz, N, pl.piece, 64, kVlK) &&
                     make_tmap_box(&wm, a.w, a.V, d, 64, kVlK) && (!a.dw || make_tmap_box(&hm, hx, N, d, 64, kVlK));
     if (!ok) return cudaErrorInvalidValue;
     VlParams p;
