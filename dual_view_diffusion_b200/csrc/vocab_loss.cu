@@ -134,19 +134,51 @@ __global__ void __launch_bounds__(kStThreads) ce_tile_simt(const T *h, const T *
     }
 }
 
-// lse and loss from the tiles' records: 32 rows x 8 strands of tiles.
-__global__ void __launch_bounds__(256) ce_finalize_kernel(const float2 *rec, const float *zt, const int32_t *targets,
-                                                          int n_tiles, int N, int V, float *loss, float *lse,
-                                                          unsigned *err)
+// lse and loss from the tiles' records: rx rows x 1024 / rx strands of tiles
+// per block (few rows: many strands, or one row's records would be read one
+// after the other).
+// EXACT (tensor-core path): the tensor cores' accumulator truncates, which
+// moves a logit by up to ~1e-5 of itself.  Over the vocabulary that averages
+// out, but the target's logit enters the loss alone, so it is taken again as
+// an fp32 dot product and replaces its first value in the sum as well.
+constexpr int kFinThreads = 1024;
+
+template <bool EXACT>
+__global__ void __launch_bounds__(kFinThreads) ce_finalize_kernel(const float2 *rec, const float *zt, LossArgs a,
+                                                                  int n_tiles, int rx)
 {
-    __shared__ float sm[8][32], ss[8][32];
+    __shared__ float sm[kFinThreads], ss[kFinThreads], sz[32];
     pdl_trigger();
     pdl_wait();
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, row = blockIdx.x * 32 + x;
+    const int N = a.N, V = a.V, strands = kFinThreads / rx;
+    const int x = threadIdx.x % rx, y = threadIdx.x / rx, row = blockIdx.x * rx + x;
+    if (EXACT) {   // one warp per row
+        const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, r = blockIdx.x * rx + w;
+        if (w < rx && r < N) {
+            const int t = a.targets[r];
+            if (t >= 0 && t < V) {
+                const uint4 *ph = (const uint4 *)((const bf16 *)a.h + (size_t)r * a.d);
+                const uint4 *pw = (const uint4 *)((const bf16 *)a.w + (size_t)t * a.d);
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                for (int i = lane; i < a.d / 8; i += 32) {
+                    const uint4 u = ph[i], v = pw[i];
+                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        acc[k] = fmaf(__uint_as_float(uu[k] << 16), __uint_as_float(vv[k] << 16), acc[k]);
+                        acc[k] = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(vv[k] & 0xffff0000u), acc[k]);
+                    }
+                }
+                const float z = warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+                if (lane == 0) sz[w] = z;
+            }
+        }
+    }
     float m = -INFINITY, s = 0.f;
     if (row < N) {
 #pragma unroll 4
-        for (int i = y; i < n_tiles; i += 8) {
+        for (int i = y; i < n_tiles; i += strands) {
             const float2 v = rec[(size_t)i * N + row];
             const float mn = fmaxf(m, v.x);
             const float sh = exp_shift(mn);
@@ -154,29 +186,45 @@ __global__ void __launch_bounds__(256) ce_finalize_kernel(const float2 *rec, con
             m = mn;
         }
     }
-    sm[y][x] = m;
-    ss[y][x] = s;
+    sm[threadIdx.x] = m;
+    ss[threadIdx.x] = s;
+    // strands join in pairs, in a fixed order
+    for (int o = strands / 2; o > 0; o >>= 1) {
+        __syncthreads();
+        if (y < o) {
+            const int q = threadIdx.x + o * rx;
+            const float m2 = sm[q], mn = fmaxf(m, m2), sh = exp_shift(mn);
+            s = s * expf(m - sh) + ss[q] * expf(m2 - sh);
+            m = mn;
+            sm[threadIdx.x] = m;
+            ss[threadIdx.x] = s;
+        }
+    }
     __syncthreads();
     if (y || row >= N) return;
-    float M = sm[0][x], S = 0.f;
-#pragma unroll
-    for (int k = 1; k < 8; ++k) M = fmaxf(M, sm[k][x]);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (ss[k][x] != 0.f) S += ss[k][x] * expf(sm[k][x] - exp_shift(M));
-    const float L = M + logf(S);
-    const int t = targets[row];
-    lse[row] = L;
-    if (t >= V && err) raise_err(err, ORTHRUS_DEVERR_TOKEN);
-    if (t < 0 || t >= V) { loss[row] = 0.f; return; }
-    if (!isfinite(L) && err) raise_err(err, ORTHRUS_DEVERR_NONFINITE);
-    loss[row] = L - zt[row];
+    const int t = a.targets[row];
+    const bool live = t >= 0 && t < V;
+    float z = live ? zt[row] : 0.f;
+    if (EXACT && live) {
+        s += expf(sz[x] - exp_shift(m)) - expf(z - exp_shift(m));
+        z = sz[x];
+    }
+    const float L = m + logf(s);
+    a.lse[row] = L;
+    if (t >= V && a.err) raise_err(a.err, ORTHRUS_DEVERR_TOKEN);
+    if (!live) { a.loss[row] = 0.f; return; }
+    if (!isfinite(L) && a.err) raise_err(a.err, ORTHRUS_DEVERR_NONFINITE);
+    a.loss[row] = L - z;
 }
 
-cudaError_t launch_ce_finalize(const float2 *rec, const float *zt, const LossArgs &a, int n_tiles, cudaStream_t s)
+cudaError_t launch_ce_finalize(const float2 *rec, const float *zt, const LossArgs &a, int n_tiles, int exact,
+                               cudaStream_t s)
 {
-    return launch_k(ce_finalize_kernel, (a.N + 31) / 32, 256, 0, s, rec, zt, a.targets, n_tiles, a.N, a.V, a.loss, a.lse,
-                    a.err);
+    int rx = 1;
+    while (rx < 32 && rx < a.N) rx <<= 1;
+    const int grid = (a.N + rx - 1) / rx;
+    return exact ? launch_k(ce_finalize_kernel<true>, grid, kFinThreads, 0, s, rec, zt, a, n_tiles, rx)
+                 : launch_k(ce_finalize_kernel<false>, grid, kFinThreads, 0, s, rec, zt, a, n_tiles, rx);
 }
 
 // dz of one piece [v0, v0 + Vp) of the vocabulary, fp32.  A row whose
@@ -372,7 +420,7 @@ template <class T> static cudaError_t loss_fwd_simt(const LossArgs &a, cudaStrea
     cudaError_t e = launch_k(ce_tile_simt<T>, dim3(nt, (a.N + kSt - 1) / kSt), kStThreads, 0, s, (const T *)a.h,
                              (const T *)a.w, a.targets, a.N, a.d, a.V, rec, zt);
     if (e != cudaSuccess) return e;
-    return launch_ce_finalize(rec, zt, a, nt, s);
+    return launch_ce_finalize(rec, zt, a, nt, 0, s);
 }
 
 template <class T> static cudaError_t loss_grad_simt(const LossArgs &a, cudaStream_t s)

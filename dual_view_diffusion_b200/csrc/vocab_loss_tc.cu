@@ -14,6 +14,11 @@
 //   DH    dh += dz W         A = dz rows, B = W read along its rows (MN-major)
 //   DW    dW  = dz^T h       both operands MN-major
 //
+// With few rows these products stream W once and little else.  LSE_T, DZ_T,
+// DZKL_T and DH_T then take W as the 256-row operand and the rows as bn
+// (32 .. 256) columns: a stage is nearly all weights, so the ring keeps up to
+// 192 KB of them in flight per SM instead of 48.
+//
 //   warp 0      producer: one thread issues the CTA's TMA loads into a ring of
 //               shared-memory stages; both CTAs' loads count on the first
 //               CTA's mbarrier
@@ -42,13 +47,15 @@ constexpr int kVlM = 256;                      // rows of a pair's tile
 constexpr int kVlNMax = 256;                   // columns of a pair's tile
 constexpr int kVlK = 128;                      // k per stage: eight MMAs for each wait and commit
 constexpr uint32_t kVlABytes = 128 * kVlK * 2; // A bytes of a CTA's stage
-constexpr int kVlStages = 3;
+constexpr int kVlStages = 6;                   // most ring stages (3 at bn = 256)
+constexpr uint32_t kVlRing = 221184;           // bytes of the ring: 3 stages of 64 KiB, or 6 at bn = 32
 constexpr int kVlPairs = 74;                   // 2-CTA clusters that fit at once on 148 SMs
 constexpr int kVlJobs = 3;
 constexpr long long kVlSpinCycles = 4000000000LL;   // ~2 s at the B200 SM clock
 constexpr float kLog2e = 1.4426950408889634f;
 
-enum VlKind : int { VL_LSE = 0, VL_DZ = 1, VL_DZKL = 2, VL_DH = 3, VL_DW = 4 };
+enum VlKind : int { VL_LSE = 0, VL_DZ = 1, VL_DZKL = 2, VL_DH = 3, VL_DW = 4, VL_LSE_T = 5, VL_DZ_T = 6, VL_DZKL_T = 7,
+                    VL_DH_T = 8 };
 
 // One product of a launch: mt x nt x splits tiles.
 struct VlJob {
@@ -57,13 +64,14 @@ struct VlJob {
     int M, N;            // valid rows and columns of the result
     int chunks, splits;  // k chunks of kVlK, and the shares they are cut into (DH)
     int bn, mt, nt;
-    int b_off;           // B's first row (K-major) or first k row (MN-major): the piece's offset in W
+    int a_mn, b_mn;      // operand order in memory: 1 = MN-major
+    int a_off, b_off;    // first row (K-major) or k row (MN-major): the piece's offset in W
     int n_fast;          // tile order: 1 = columns first, 0 = rows first
     // epilogue
     const int32_t *targets;
     const float *lse, *lse2, *g;
-    float2 *rec;         // LSE: [nt][M]
-    float *zt;           // LSE: [M]
+    float2 *rec;         // LSE: [nt][M]; LSE_T: [groups of 32 ids][N]
+    float *zt;           // LSE: the rows' target logits
     bf16 *dz;            // DZ: [rows][pitch]
     int v0, V, pitch;    // DZ: the piece's first id, the vocabulary, dz's row length
     float *part;         // DH: [splits][M][N] fp32
@@ -72,7 +80,8 @@ struct VlJob {
 };
 struct VlParams {
     VlJob job[kVlJobs];
-    int jobs, pairs;
+    int jobs, pairs, stages;
+    uint32_t stage_bytes;
     unsigned *err;
     // job 0: tiles p, p + pairs, ..; job j > 0: tiles [first[j][p], first[j][p + 1])
     uint16_t first[kVlJobs][kVlPairs + 1];
@@ -108,7 +117,7 @@ __device__ __forceinline__ bool vl_wait(uint64_t *b, uint32_t parity, volatile i
     const long long t0 = clock64();
     for (long i = 0;; ++i) {
         if (vl_try(b, parity)) return true;
-        if ((i & 255) == 255) {
+        if ((i & 15) == 15) {   // (a try may itself be suspended for a while)
             if (*abort) return false;
             if (clock64() - t0 > kVlSpinCycles) break;
         }
@@ -163,11 +172,12 @@ __device__ __forceinline__ void vl_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void vl_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void vl_cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+    asm volatile("barrier.cluster.arrive;\nbarrier.cluster.wait;\n" ::: "memory");
 }
 __device__ __forceinline__ void vl_tmem_ld32(uint32_t taddr, float (&r)[32])
 {
     uint32_t u[32];
+    __syncwarp();   // (lanes without a row to write skip the previous chunk's stores)
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
@@ -237,6 +247,9 @@ struct VlSmem {
     alignas(8) uint64_t full[kVlStages], empty[kVlStages], tfull[2], tempty[2];
     uint32_t tmem_base;
     int abort;
+    // transposed kinds: per column (row of h) lse * log2 e, upstream gradient, target
+    float col_k[kVlNMax], col_g[kVlNMax];
+    int col_t[kVlNMax];
 };
 
 // ---------------------------------------------------------------- epilogues
@@ -384,6 +397,120 @@ __device__ __forceinline__ void vl_epi_dw(const VlJob &jb, const VlTile &x, int 
     }
 }
 
+// ---- transposed: a thread holds one id (or one hidden column), 32 rows at a time
+// the columns' constants, one column per thread
+__device__ __forceinline__ void vl_columns(const VlJob &jb, VlSmem &sm, unsigned *err)
+{
+    const int c = threadIdx.x;
+    float k = 0.f, g = 0.f;
+    int t = -1;
+    if (c < jb.N) {
+        if (jb.kind == VL_DZKL_T) {
+            k = (c & 1 ? jb.lse2 : jb.lse)[c >> 1] * kLog2e;
+            g = jb.g[c >> 1];
+        } else {
+            k = jb.lse[c] * kLog2e;
+            t = jb.targets[c];
+            if (t >= 0 && t < jb.V) g = jb.g[c];
+            if (t >= jb.V && blockIdx.x == 0 && err) raise_err(err, ORTHRUS_DEVERR_TOKEN);
+        }
+    }
+    sm.col_k[c] = k;
+    sm.col_g[c] = g;
+    sm.col_t[c] = t;
+}
+static_assert(kVlThreads == kVlNMax, "one column per thread");
+
+__device__ __forceinline__ float warp_max_f32(float v)
+{
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(m) : "f"(v));
+    return m;
+}
+
+// v: this thread's id (the tile's ids are in order, so a warp holds one group
+// of 32); a record per (group, row).
+__device__ __forceinline__ void vl_epi_lse_t(const VlJob &jb, int v, uint32_t taddr, int lane)
+{
+    for (int c = 0; c < jb.N; c += 32) {
+        float r[32], m = -INFINITY;
+        vl_tmem_ld32(taddr + c, r);
+        const int tgt = c + lane < jb.N ? jb.targets[c + lane] : -1;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (v >= jb.M) r[j] = -INFINITY;
+            const int t = __shfl_sync(0xffffffffu, tgt, j);
+            if (t == v && v < jb.M) jb.zt[c + j] = r[j];
+            const float mj = warp_max_f32(r[j]), k = (mj == -INFINITY ? 0.f : mj) * kLog2e;
+            r[j] = vl_exp2(fmaf(r[j], kLog2e, -k));
+            if (lane == j) m = mj;
+        }
+        // lane j ends with the sum of column j
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < o; ++i) {
+                const float keep = lane & o ? r[i + o] : r[i], send = lane & o ? r[i] : r[i + o];
+                r[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        if (c + lane < jb.N) jb.rec[(size_t)(v / 32) * jb.N + c + lane] = make_float2(m, r[0]);
+    }
+}
+
+// i: this thread's id within the piece; jb.M ids of the piece are real, the
+// rest of dz's row length gets zeros
+__device__ __forceinline__ void vl_epi_dz_t(const VlJob &jb, const VlSmem &sm, int i, uint32_t taddr)
+{
+    const int v = jb.v0 + i;
+    const bool live = i < jb.M;
+    for (int c = 0; c < jb.N; c += 32) {
+        float r[32];
+        vl_tmem_ld32(taddr + c, r);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (c + j >= jb.N) break;
+            const float g = sm.col_g[c + j];
+            float e = vl_exp2(fmaf(r[j], kLog2e, -sm.col_k[c + j]));
+            if (sm.col_t[c + j] == v) e -= 1.f;
+            jb.dz[(size_t)(c + j) * jb.pitch + i] = __float2bfloat16_rn(g == 0.f || !live ? 0.f : g * e);
+        }
+    }
+}
+
+__device__ __forceinline__ void vl_epi_dzkl_t(const VlJob &jb, const VlSmem &sm, int i, uint32_t taddr)
+{
+    const bool live = i < jb.M;
+    for (int c = 0; c < jb.N; c += 32) {
+        float r[32];
+        vl_tmem_ld32(taddr + c, r);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            if (c + j >= jb.N) break;
+            const float g = sm.col_g[c + j];
+            const float pa = vl_exp2(fmaf(r[j], kLog2e, -sm.col_k[c + j]));
+            const float pd = vl_exp2(fmaf(r[j + 1], kLog2e, -sm.col_k[c + j + 1]));
+            jb.dz[(size_t)((c + j) >> 1) * jb.pitch + i] = __float2bfloat16_rn(g == 0.f || !live ? 0.f : g * (pd - pa));
+        }
+    }
+}
+
+__device__ __forceinline__ void vl_epi_dh_t(const VlJob &jb, const VlTile &x, int i, uint32_t taddr)
+{
+    for (int c = 0; c < jb.N; c += 32) {
+        float r[32];
+        vl_tmem_ld32(taddr + c, r);
+        if (i >= jb.M) continue;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (c + j >= jb.N) break;
+            float *p = jb.part + ((size_t)x.split * jb.N + c + j) * jb.M + i;
+            const float s = jb.add ? *p + r[j] : r[j];
+            if (jb.last) jb.out[(size_t)(c + j) * jb.M + i] = __float2bfloat16_rn(s);
+            else *p = s;
+        }
+    }
+}
+
 // ---------------------------------------------------------------- kernel
 __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_constant__ VlParams prm)
 {
@@ -394,7 +521,6 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
     const uint32_t rank = blockIdx.x & 1;               // CTA of the pair
     const int pair = blockIdx.x >> 1;
     volatile int *abort = &sm.abort;
-    constexpr uint32_t kStage = kVlABytes + kVlNMax / 2 * kVlK * 2;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kVlStages; ++s) { vl_mbar_init(&sm.full[s], 1); vl_mbar_init(&sm.empty[s], 1); }
@@ -413,6 +539,11 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
     vl_fence_after();
     const uint32_t tmem = sm.tmem_base;
     pdl_wait();
+    for (int j = 0; j < prm.jobs; ++j)   // (at most one job of a launch has columns)
+        if (prm.job[j].kind == VL_DZ_T || prm.job[j].kind == VL_DZKL_T) {
+            vl_columns(prm.job[j], sm, prm.err);
+            __syncthreads();
+        }
 
     if (warp == 0) {
         if (lane == 0) {   // ------------------------------------------- producer
@@ -427,23 +558,23 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
                     if (!vl_wait(&sm.empty[stage], phase ^ 1, abort) || *abort) { stop = true; break; }
                     if (rank == 0) vl_expect_tx(&sm.full[stage], bytes);
                     const uint32_t bar = vl_mapa(smem_u32(&sm.full[stage]), 0);
-                    const uint32_t a = ring + stage * kStage, b = a + kVlABytes;
+                    const uint32_t a = ring + stage * prm.stage_bytes, b = a + kVlABytes;
                     const int k = c * kVlK;
                     // two boxes of 64 elements each: along k (K-major), or along M / N
-                    if (jb.kind == VL_DW) {
-                        vl_load(a, &jb.a, am, k, bar);
-                        vl_load(a + kVlABytes / 2, &jb.a, am + 64, k, bar);
+                    if (jb.a_mn) {
+                        vl_load(a, &jb.a, am, jb.a_off + k, bar);
+                        vl_load(a + kVlABytes / 2, &jb.a, am + 64, jb.a_off + k, bar);
                     } else {
-                        vl_load(a, &jb.a, k, am, bar);
-                        vl_load(a + kVlABytes / 2, &jb.a, k + 64, am, bar);
+                        vl_load(a, &jb.a, k, jb.a_off + am, bar);
+                        vl_load(a + kVlABytes / 2, &jb.a, k + 64, jb.a_off + am, bar);
                     }
-                    if (jb.kind >= VL_DH) {
+                    if (jb.b_mn) {
                         for (int q = 0; q < bnh; q += 64) vl_load(b + q * kVlK * 2, &jb.b, bx + q, jb.b_off + k, bar);
                     } else {
                         vl_load(b, &jb.b, k, jb.b_off + bx, bar);
                         vl_load(b + bnh * 128, &jb.b, k + 64, jb.b_off + bx, bar);
                     }
-                    if (++stage == (uint32_t)kVlStages) { stage = 0; phase ^= 1; }
+                    if (++stage == (uint32_t)prm.stages) { stage = 0; phase ^= 1; }
                 }
             }
             pdl_trigger();
@@ -457,7 +588,7 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
                 const VlJob &jb = prm.job[it.j];
                 const VlTile x = it.get();
                 const int acc = local & 1;
-                const bool a_mn = jb.kind == VL_DW, b_mn = jb.kind >= VL_DH;
+                const bool a_mn = jb.a_mn, b_mn = jb.b_mn;
                 const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
                                        ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(jb.bn >> 3) << 17) |
                                        ((uint32_t)(kVlM >> 4) << 24);
@@ -471,14 +602,14 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
                 for (int c = x.c0; c < x.c1; ++c) {
                     if (!vl_wait(&sm.full[stage], phase, abort)) { ok = false; break; }
                     vl_fence_after();
-                    const uint32_t a = ring + stage * kStage, b = a + kVlABytes;
+                    const uint32_t a = ring + stage * prm.stage_bytes, b = a + kVlABytes;
                     const uint64_t ad = a_mn ? vl_desc_mn(a) : vl_desc_k(a), bd = b_mn ? vl_desc_mn(b) : vl_desc_k(b);
 #pragma unroll
                     for (int k = 0; k < kVlK / 16; ++k)
                         vl_mma(d, ad + as * (k & 3) + ah * (k >> 2), bd + bs * (k & 3) + bh * (k >> 2), idesc,
                                (c > x.c0 || k > 0) ? 1u : 0u);
                     vl_commit(&sm.empty[stage]);
-                    if (++stage == (uint32_t)kVlStages) { stage = 0; phase ^= 1; }
+                    if (++stage == (uint32_t)prm.stages) { stage = 0; phase ^= 1; }
                 }
                 if (!ok) break;
                 vl_commit(&sm.tfull[acc]);
@@ -498,13 +629,19 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
             if (!__all_sync(0xffffffffu, ok)) break;
             vl_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kVlNMax;
-            if (x.m0 + (int)rank * 128 + q * 32 < jb.M) {   // (whole warps past the last row have nothing to do)
+            // (whole warps past the last row have nothing to do, but dz's padding is written)
+            const int rows = jb.kind == VL_DZ_T || jb.kind == VL_DZKL_T ? jb.pitch : jb.M;
+            if (x.m0 + (int)rank * 128 + q * 32 < rows) {
                 switch (jb.kind) {
                 case VL_LSE: vl_epi_lse(jb, x, row, taddr); break;
                 case VL_DZ: vl_epi_dz(jb, x, row, taddr, prm.err); break;
                 case VL_DZKL: vl_epi_dzkl(jb, x, row, taddr); break;
                 case VL_DH: vl_epi_dh(jb, x, row, taddr); break;
-                default: vl_epi_dw(jb, x, row, taddr); break;
+                case VL_DW: vl_epi_dw(jb, x, row, taddr); break;
+                case VL_LSE_T: vl_epi_lse_t(jb, row, taddr, lane); break;
+                case VL_DZ_T: vl_epi_dz_t(jb, sm, row, taddr); break;
+                case VL_DZKL_T: vl_epi_dzkl_t(jb, sm, row, taddr); break;
+                default: vl_epi_dh_t(jb, x, row, taddr); break;
                 }
             }
             vl_fence_before();
@@ -546,19 +683,11 @@ __global__ void __launch_bounds__(256) vl_interleave_kernel(const uint4 *ra, con
 // ---------------------------------------------------------------- host
 static size_t up(size_t x, size_t m) { return (x + m - 1) / m * m; }
 
-// Columns per tile of z: 256, unless a single row tile leaves so few tiles
-// that whole rounds of the pairs waste more than narrower tiles do.
-static int vl_bn(int rows, long cols)
-{
-    if (rows > kVlM) return kVlNMax;
-    int best = kVlNMax;
-    long cost = -1;
-    for (int bn = kVlNMax; bn >= 128; bn -= 128) {   // (a multiple of dh's k chunk)
-        const long t = ((cols + bn - 1) / bn + kVlPairs - 1) / kVlPairs * (bn + 8);
-        if (cost < 0 || t < cost) { cost = t; best = bn; }
-    }
-    return best;
-}
+// Up to kVlNMax rows ride as columns beside W's rows: a stage is then mostly
+// weights (measured at one row of 2048, vocabulary 151936: the 256-row tile of
+// h kept 48 KB of W in flight per SM and ran at 285 us, this one at ~110).
+static bool vl_narrow(int rows) { return rows <= kVlNMax; }
+static int vl_narrow_bn(int rows) { return (rows + 31) / 32 * 32; }
 
 // Shares of dh's k axis: the smallest count that keeps the rounds of the
 // pairs nearly full, each share at least 4 chunks.
@@ -582,9 +711,15 @@ bool loss_tc_ok(const LossArgs &a)
 static cudaError_t vl_launch(VlParams &p, cudaStream_t s)
 {
     long tiles = 0;
-    for (int j = 0; j < p.jobs; ++j) tiles += (long)p.job[j].mt * p.job[j].nt * p.job[j].splits;
+    int bn = 0;
+    for (int j = 0; j < p.jobs; ++j) {
+        tiles += (long)p.job[j].mt * p.job[j].nt * p.job[j].splits;
+        bn = std::max(bn, p.job[j].bn);
+    }
     p.pairs = (int)std::min<long>(kVlPairs, tiles);
-    const size_t smem = 1024 + (size_t)kVlStages * (kVlABytes + kVlNMax / 2 * kVlK * 2);
+    p.stage_bytes = kVlABytes + (uint32_t)bn / 2 * kVlK * 2;
+    p.stages = (int)std::min<uint32_t>(kVlStages, kVlRing / p.stage_bytes);
+    const size_t smem = 1024 + kVlRing;
     cudaError_t e = cudaFuncSetAttribute(vocab_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -607,33 +742,37 @@ static cudaError_t vl_launch(VlParams &p, cudaStream_t s)
 size_t loss_fwd_workspace_tc(int N, int d, int V)
 {
     WsPlan w;
-    w.take((size_t)((V + 127) / 128) * N * sizeof(float2));
+    w.take((size_t)(vl_narrow(N) ? (V + 31) / 32 : (V + kVlNMax - 1) / kVlNMax) * N * sizeof(float2));
     w.take((size_t)N * 4);
     return w.total;
 }
 
 cudaError_t loss_fwd_tc(const LossArgs &a, cudaStream_t s)
 {
-    WsPlan w;
-    float2 *rec = (float2 *)(a.ws + w.take((size_t)((a.V + 127) / 128) * a.N * sizeof(float2)));
-    float *zt = (float *)(a.ws + w.take((size_t)a.N * 4));
+    float2 *rec = (float2 *)a.ws;
+    float *zt = (float *)(a.ws + loss_fwd_workspace_tc(a.N, a.d, a.V) - (((size_t)a.N * 4 + 255) & ~(size_t)255));
     VlParams p;
     memset(&p, 0, sizeof(p));
     VlJob &j = p.job[0];
-    j.kind = VL_LSE; j.M = a.N; j.N = a.V; j.chunks = (a.d + kVlK - 1) / kVlK; j.splits = 1;
-    j.bn = vl_bn(a.N, a.V); j.mt = (a.N + kVlM - 1) / kVlM; j.nt = (a.V + j.bn - 1) / j.bn;
+    const bool narrow = vl_narrow(a.N);
+    const int rows = narrow ? a.V : a.N, cols = narrow ? a.N : a.V;
+    j.kind = narrow ? VL_LSE_T : VL_LSE; j.M = rows; j.N = cols; j.chunks = (a.d + kVlK - 1) / kVlK; j.splits = 1;
+    j.bn = narrow ? vl_narrow_bn(a.N) : kVlNMax;
+    j.mt = (rows + kVlM - 1) / kVlM; j.nt = (cols + j.bn - 1) / j.bn;
     j.targets = a.targets; j.rec = rec; j.zt = zt;
-    if (!make_tmap_box(&j.a, a.h, a.N, a.d, 64, 128) || !make_tmap_box(&j.b, a.w, a.V, a.d, 64, j.bn / 2))
+    if (!make_tmap_box(&j.a, narrow ? a.w : a.h, rows, a.d, 64, 128) ||
+        !make_tmap_box(&j.b, narrow ? a.h : a.w, cols, a.d, 64, j.bn / 2))
         return cudaErrorInvalidValue;
     p.jobs = 1; p.err = a.err;
     cudaError_t e = vl_launch(p, s);
     if (e != cudaSuccess) return e;
-    return launch_ce_finalize(rec, zt, a, j.nt, s);
+    return launch_ce_finalize(rec, zt, a, narrow ? (a.V + 31) / 32 : j.nt, 1, s);
 }
 
 struct VlPlan {
     size_t total, o_dz, o_part, o_h;
-    int piece, splits, bn, zrows;
+    int piece, splits, zrows;
+    bool z_narrow, h_narrow;
 };
 static VlPlan vl_plan(int N, int d, int V, int want_dw, int kl)
 {
@@ -644,8 +783,9 @@ static VlPlan vl_plan(int N, int d, int V, int want_dw, int kl)
     const size_t cap = std::max<size_t>(256, ((size_t)128 << 20) / (2 * (size_t)N) / 256 * 256);
     p.piece = (int)std::min(cap, up(V, 256));
     p.zrows = kl ? 2 * N : N;
-    p.bn = vl_bn(p.zrows, std::min(p.piece, V));
-    const long tiles = (long)up(N, kVlM) / kVlM * ((d + 255) / 256);
+    p.z_narrow = vl_narrow(p.zrows);
+    p.h_narrow = vl_narrow(N);
+    const long tiles = p.h_narrow ? (d + kVlM - 1) / kVlM : (long)up(N, kVlM) / kVlM * ((d + 255) / 256);
     p.splits = vl_splits(tiles, (std::min(p.piece, V) + kVlK - 1) / kVlK);
     p.o_dz = w.take((size_t)N * p.piece * 2);
     p.o_part = w.take((size_t)p.splits * N * d * 4);
@@ -668,11 +808,15 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
     else if (a.dw)
         e = launch_clean_rows(a, hx, s);
     if (e != cudaSuccess) return e;
+    const int zbn = pl.z_narrow ? vl_narrow_bn(pl.zrows) : kVlNMax, hbn = pl.h_narrow ? vl_narrow_bn(N) : kVlNMax;
+    // zh: hidden rows, zw: head rows (both along k); dzk: dz along its ids; wm:
+    // head columns; dzm, hm: dz's and h's columns (dW)
     CUtensorMap zh, zw, dzk, dzm, wm, hm;
-    const bool ok = make_tmap_box(&zh, a.kl ? (const void *)hx : a.h, pl.zrows, d, 64, 128) &&
-                    make_tmap_box(&zw, a.w, a.V, d, 64, pl.bn / 2) &&
-                    make_tmap_box(&dzk, dz, N, pl.piece, 64, 128) && make_tmap_box(&dzm, dz, N, pl.piece, 64, kVlK) &&
-                    make_tmap_box(&wm, a.w, a.V, d, 64, kVlK) && (!a.dw || make_tmap_box(&hm, hx, N, d, 64, kVlK));
+    const bool ok = make_tmap_box(&zh, a.kl ? (const void *)hx : a.h, pl.zrows, d, 64, pl.z_narrow ? zbn / 2 : 128) &&
+                    make_tmap_box(&zw, a.w, a.V, d, 64, 128) &&
+                    make_tmap_box(&dzk, dz, N, pl.piece, 64, pl.h_narrow ? hbn / 2 : 128) &&
+                    make_tmap_box(&wm, a.w, a.V, d, 64, kVlK) &&
+                    (!a.dw || (make_tmap_box(&dzm, dz, N, pl.piece, 64, kVlK) && make_tmap_box(&hm, hx, N, d, 64, kVlK)));
     if (!ok) return cudaErrorInvalidValue;
     VlParams p;
     for (int v0 = 0; v0 < a.V; v0 += pl.piece) {
@@ -680,22 +824,28 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
         {
             memset(&p, 0, sizeof(p));
             VlJob &j = p.job[0];
-            j.kind = a.kl ? VL_DZKL : VL_DZ; j.M = pl.zrows; j.N = nv; j.chunks = (d + kVlK - 1) / kVlK; j.splits = 1;
-            j.bn = pl.bn; j.mt = (pl.zrows + kVlM - 1) / kVlM; j.nt = (nv + j.bn - 1) / j.bn;
-            j.b_off = v0; j.targets = a.targets; j.lse = a.lse_in; j.lse2 = a.lse2_in; j.g = a.g;
+            j.kind = a.kl ? (pl.z_narrow ? VL_DZKL_T : VL_DZKL) : (pl.z_narrow ? VL_DZ_T : VL_DZ);
+            j.M = pl.z_narrow ? nv : pl.zrows; j.N = pl.z_narrow ? pl.zrows : nv;
+            j.chunks = (d + kVlK - 1) / kVlK; j.splits = 1; j.bn = zbn;
+            j.mt = (j.M + kVlM - 1) / kVlM; j.nt = (j.N + zbn - 1) / zbn;
+            (pl.z_narrow ? j.a_off : j.b_off) = v0;
+            j.targets = a.targets; j.lse = a.lse_in; j.lse2 = a.lse2_in; j.g = a.g;
             j.dz = dz; j.v0 = v0; j.V = a.V; j.pitch = pl.piece;
-            j.a = zh; j.b = zw;
+            j.a = pl.z_narrow ? zw : zh; j.b = pl.z_narrow ? zh : zw;
             p.jobs = 1; p.err = a.err;
             if ((e = vl_launch(p, s)) != cudaSuccess) return e;
         }
         {
             memset(&p, 0, sizeof(p));
             VlJob &j = p.job[0];
-            j.kind = VL_DH; j.M = N; j.N = d; j.chunks = (nv + kVlK - 1) / kVlK;
+            j.kind = pl.h_narrow ? VL_DH_T : VL_DH;
+            j.M = pl.h_narrow ? d : N; j.N = pl.h_narrow ? N : d; j.chunks = (nv + kVlK - 1) / kVlK;
             j.splits = std::min(pl.splits, j.chunks);
-            j.bn = 256; j.mt = (N + kVlM - 1) / kVlM; j.nt = (d + 255) / 256;
-            j.b_off = v0; j.part = part; j.add = v0 > 0; j.last = pl.splits == 1 && v0 + pl.piece >= a.V; j.out = (bf16 *)a.dh;
-            j.a = dzk; j.b = wm;
+            j.bn = hbn; j.mt = (j.M + kVlM - 1) / kVlM; j.nt = (j.N + hbn - 1) / hbn;
+            (pl.h_narrow ? j.a_mn : j.b_mn) = 1;
+            (pl.h_narrow ? j.a_off : j.b_off) = v0;
+            j.part = part; j.add = v0 > 0; j.last = pl.splits == 1 && v0 + pl.piece >= a.V; j.out = (bf16 *)a.dh;
+            j.a = pl.h_narrow ? wm : dzk; j.b = pl.h_narrow ? dzk : wm;
             p.jobs = 1; p.err = a.err;
             if ((e = vl_launch(p, s)) != cudaSuccess) return e;
         }
@@ -704,6 +854,7 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
             VlJob &j = p.job[0];
             j.kind = VL_DW; j.M = nv; j.N = d; j.chunks = (N + kVlK - 1) / kVlK; j.splits = 1;
             j.bn = 256; j.mt = (nv + kVlM - 1) / kVlM; j.nt = (d + 255) / 256; j.n_fast = 1;
+            j.a_mn = j.b_mn = 1;
             j.out = (bf16 *)a.dw + (size_t)v0 * d;
             j.a = dzm; j.b = hm;
             p.jobs = 1; p.err = a.err;
