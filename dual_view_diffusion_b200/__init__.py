@@ -182,12 +182,16 @@ def _need(x, dtype, name):
 _DT = None      # torch dtype -> orthrus_dtype_t
 
 
-def _dtype_id(name, t):
+def _dtypes():
     global _DT
     if _DT is None:
         import torch
         _DT = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
-    d = _DT.get(t)
+    return _DT
+
+
+def _dtype_id(name, t):
+    d = _dtypes().get(t)
     if d is None:
         raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, got {t}")
     return d
@@ -195,16 +199,20 @@ def _dtype_id(name, t):
 
 def _need_rows(name, x, dtypes, shape, device=None):
     """A contiguous CUDA tensor of one of `dtypes` and of `shape` (None: any
-    extent), on `device` when given."""
+    extent the C entry can hold), on `device` when given; its shape."""
     if not x.is_cuda or not x.is_contiguous() or x.dtype not in dtypes:
         raise TypeError(f"{name}: expected a contiguous CUDA tensor of {' or '.join(str(d) for d in dtypes)}, got "
                         f"{x.dtype} on {x.device}{'' if x.is_contiguous() else ', not contiguous'}")
     if device is not None and x.device != device:
         raise ValueError(f"{name}: on {x.device}, the other arguments on {device}")
-    if x.dim() != len(shape) or any(s is not None and int(n) != s for n, s in zip(x.shape, shape)):
-        raise ValueError(f"{name}: expected shape {tuple('*' if s is None else s for s in shape)}, got "
-                         f"{tuple(int(n) for n in x.shape)}")
-    return x
+    have = x.shape
+    if len(have) != len(shape):
+        raise ValueError(f"{name}: expected {len(shape)} dimensions, got {len(have)}")
+    for n, s in zip(have, shape):
+        if n != s and (s is not None or n >= 1 << 31):
+            raise ValueError(f"{name}: expected shape {tuple('*' if q is None else q for q in shape)} (extents below "
+                             f"2^31), got {tuple(have)}")
+    return have
 
 
 class _OnDevice:
@@ -212,13 +220,14 @@ class _OnDevice:
 
     def __init__(self, device):
         import torch
-        self.torch = torch
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.index = device.index
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+        self.guard = None if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        return C.c_void_p(self.torch.cuda.current_stream().cuda_stream)
+        return self.raw_stream(self.index)
 
     def __exit__(self, *exc):
         if self.guard is not None:
@@ -249,13 +258,11 @@ def orthrus_embed_rows(table, ids, scale=1.0, out_dtype=None, err=None):
     [rows] (negative: a zero row).  Returns [rows, hidden] of out_dtype (default
     fp32, the residual stream's)."""
     import torch
-    _need_rows("table", table, (torch.bfloat16, torch.float32), (None, None))
+    V, d = _need_rows("table", table, _dtypes(), (None, None))
     dev = table.device
-    _need_rows("ids", ids, (torch.int32,), (None,), dev)
+    n, = _need_rows("ids", ids, (torch.int32,), (None,), dev)
     out_dtype = torch.float32 if out_dtype is None else out_dtype
     od = _dtype_id("out_dtype", out_dtype)
-    V, d = table.shape
-    n = ids.shape[0]
     with _OnDevice(dev) as stream:
         out = torch.empty((n, d), dtype=out_dtype, device=dev)
         _check("orthrus_embed_rows", lib().orthrus_embed_rows(
@@ -269,22 +276,24 @@ def orthrus_embed_grad(dout, ids, vocab, scale=1.0, dtype=None, out=None, accumu
     (default dout's), zeros for ids that do not occur.  With `out` the result is
     written there, or added to it when accumulate is set."""
     import torch
-    fl = (torch.bfloat16, torch.float32)
-    _need_rows("dout", dout, fl, (None, None))
+    fl = _dtypes()
+    n, d = _need_rows("dout", dout, fl, (None, None))
     dev = dout.device
-    n, d = dout.shape
     _need_rows("ids", ids, (torch.int32,), (n,), dev)
+    vocab = int(vocab)
+    if not 0 < vocab < 1 << 31:
+        raise ValueError(f"vocab: expected 1 .. 2^31 - 1, got {vocab}")
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if out is not None:
-        _need_rows("out", out, fl if dtype is None else (dtype,), (int(vocab), d), dev)
+        _need_rows("out", out, fl if dtype is None else (dtype,), (vocab, d), dev)
     with _OnDevice(dev) as stream:
         if out is None:
-            out = torch.empty((int(vocab), d), dtype=dout.dtype if dtype is None else dtype, device=dev)
+            out = torch.empty((vocab, d), dtype=dout.dtype if dtype is None else dtype, device=dev)
         od = _dtype_id("dtype", out.dtype)
-        ws, wp, wn = _train_ws("orthrus_embed_grad_workspace", dev, n, d, int(vocab))
+        ws, wp, wn = _train_ws("orthrus_embed_grad_workspace", dev, n, d, vocab)
         _check("orthrus_embed_grad", lib().orthrus_embed_grad(
-            _ptr(dout), _dtype_id("dout", dout.dtype), _ptr(ids), n, d, int(vocab), float(scale), int(bool(accumulate)),
+            _ptr(dout), _dtype_id("dout", dout.dtype), _ptr(ids), n, d, vocab, float(scale), int(bool(accumulate)),
             _ptr(out), od, wp, wn, _err_ptr(err, dev), stream))
     return out
 
@@ -293,10 +302,8 @@ def orthrus_rmsnorm(x, gain, eps):
     """x * gain / sqrt(mean(x^2) + eps) per row: x [rows, hidden] fp32 or gain's
     dtype; the result has gain's dtype."""
     import torch
-    fl = (torch.bfloat16, torch.float32)
-    _need_rows("x", x, fl, (None, None))
-    n, d = x.shape
-    _need_rows("gain", gain, fl, (d,), x.device)
+    n, d = _need_rows("x", x, _dtypes(), (None, None))
+    _need_rows("gain", gain, _dtypes(), (d,), x.device)
     with _OnDevice(x.device) as stream:
         y = torch.empty((n, d), dtype=gain.dtype, device=x.device)
         _check("orthrus_rmsnorm", lib().orthrus_rmsnorm(
@@ -309,11 +316,9 @@ def orthrus_rmsnorm_grad(x, gain, dy, eps):
     """Gradient of orthrus_rmsnorm: (dx [rows, hidden] of x's dtype, dgain fp32
     [hidden])."""
     import torch
-    fl = (torch.bfloat16, torch.float32)
-    _need_rows("x", x, fl, (None, None))
+    n, d = _need_rows("x", x, _dtypes(), (None, None))
     dev = x.device
-    n, d = x.shape
-    _need_rows("gain", gain, fl, (d,), dev)
+    _need_rows("gain", gain, _dtypes(), (d,), dev)
     _need_rows("dy", dy, (gain.dtype,), (n, d), dev)
     with _OnDevice(dev) as stream:
         dx = torch.empty_like(x)
@@ -330,12 +335,11 @@ def orthrus_ce_lm_head(h, w, targets, err=None):
     [rows, hidden] (same dtype): (loss, lse), fp32 [rows].  targets int32
     [rows]; negative: an ignored row (loss 0)."""
     import torch
-    _need_rows("h", h, (torch.bfloat16, torch.float32), (None, None))
+    n, d = _need_rows("h", h, _dtypes(), (None, None))
     dev = h.device
-    n, d = h.shape
-    _need_rows("w", w, (h.dtype,), (None, d), dev)
+    V, _ = _need_rows("w", w, (h.dtype,), (None, d), dev)
     _need_rows("targets", targets, (torch.int32,), (n,), dev)
-    V, dt = w.shape[0], _dtype_id("h", h.dtype)
+    dt = _dtype_id("h", h.dtype)
     with _OnDevice(dev) as stream:
         loss = torch.empty(n, dtype=torch.float32, device=dev)
         lse = torch.empty_like(loss)
@@ -349,14 +353,13 @@ def orthrus_ce_lm_head_grad(h, w, targets, lse, dloss, weight_grad=True, err=Non
     """Gradient of orthrus_ce_lm_head from its lse and the upstream dloss (fp32
     [rows]): (dh [rows, hidden], dw [vocab, hidden] or None), h's dtype."""
     import torch
-    _need_rows("h", h, (torch.bfloat16, torch.float32), (None, None))
+    n, d = _need_rows("h", h, _dtypes(), (None, None))
     dev = h.device
-    n, d = h.shape
-    _need_rows("w", w, (h.dtype,), (None, d), dev)
+    V, _ = _need_rows("w", w, (h.dtype,), (None, d), dev)
     _need_rows("targets", targets, (torch.int32,), (n,), dev)
     _need_rows("lse", lse, (torch.float32,), (n,), dev)
     _need_rows("dloss", dloss, (torch.float32,), (n,), dev)
-    V, dt = w.shape[0], _dtype_id("h", h.dtype)
+    dt = _dtype_id("h", h.dtype)
     with _OnDevice(dev) as stream:
         dh = torch.empty_like(h)
         dw = torch.empty_like(w) if weight_grad else None
@@ -372,14 +375,13 @@ def orthrus_kl_lm_head_grad(h_ar, h_diff, w, lse_ar, lse_diff, dkl, err=None):
     h_diff, from both log-sum-exps and the upstream dkl (fp32 [rows]): dh_diff
     [rows, hidden], h_diff's dtype."""
     import torch
-    _need_rows("h_ar", h_ar, (torch.bfloat16, torch.float32), (None, None))
+    n, d = _need_rows("h_ar", h_ar, _dtypes(), (None, None))
     dev = h_ar.device
-    n, d = h_ar.shape
     _need_rows("h_diff", h_diff, (h_ar.dtype,), (n, d), dev)
-    _need_rows("w", w, (h_ar.dtype,), (None, d), dev)
+    V, _ = _need_rows("w", w, (h_ar.dtype,), (None, d), dev)
     for name, x in (("lse_ar", lse_ar), ("lse_diff", lse_diff), ("dkl", dkl)):
         _need_rows(name, x, (torch.float32,), (n,), dev)
-    V, dt = w.shape[0], _dtype_id("h_ar", h_ar.dtype)
+    dt = _dtype_id("h_ar", h_ar.dtype)
     with _OnDevice(dev) as stream:
         dh = torch.empty_like(h_diff)
         ws, wp, wn = _train_ws("orthrus_kl_lm_head_grad_workspace", dev, n, d, V, dt)
