@@ -38,7 +38,7 @@ constexpr int kSortTile = 2048;    // keys per block of the radix sort
 constexpr int kSortDigit = 9;      // widest radix digit
 
 struct EmbedGradPlan {
-    size_t total, o_tok[2], o_idx[2], o_hist, o_part;
+    size_t total, o_tok[2], o_idx[2], o_hist, o_part, o_bits;
     int piece;     // sorted rows per piece
     int pieces;
     int digits, digit_bits, tiles;   // radix sort (rows > kSortSmall)

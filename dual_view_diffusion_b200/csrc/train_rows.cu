@@ -53,6 +53,17 @@ template <> struct RowVec<bf16, 8> {
     }
 };
 
+// Zeros in [p, p + bytes) by the n threads t = 0 .. n - 1 (p and bytes even).
+__device__ __forceinline__ void zero_span(char *p, size_t bytes, size_t t, size_t n)
+{
+    char *a = (char *)(((uintptr_t)p + 15) & ~(uintptr_t)15), *e = p + bytes;
+    if (a > e) a = e;
+    char *b = a + (size_t)(e - a) / 16 * 16;
+    for (char *q = p + 2 * t; q < a; q += 2 * n) *(uint16_t *)q = 0;
+    for (char *q = a + 16 * t; q < b; q += 16 * n) *(uint4 *)q = make_uint4(0, 0, 0, 0);
+    for (char *q = b + 2 * t; q < e; q += 2 * n) *(uint16_t *)q = 0;
+}
+
 static bool rows_aligned(const void *p, int d) { return ((uintptr_t)p & 15) == 0 && d % 8 == 0; }
 
 // ---------------------------------------------------------------- embedding
@@ -146,6 +157,7 @@ EmbedGradPlan plan_embed_grad(int rows, int vocab, int d)
     while (p.piece < 4096 && rows / p.piece > 1024) p.piece *= 2;
     p.pieces = (rows + p.piece - 1) / p.piece;
     p.o_part = w.take((size_t)p.pieces * 2 * d * 4);
+    p.o_bits = w.take(((size_t)vocab + 31) / 32 * 4);
     p.total = w.total;
     return p;
 }
@@ -157,52 +169,113 @@ __device__ __forceinline__ int sort_key(const int32_t *ids, int r, int vocab, un
     return id < 0 || id >= vocab ? vocab : id;
 }
 
-// Zeros of the whole gradient (the rows of tokens that do not occur), by
-// blocks first .. of the launch.
-__device__ __forceinline__ void fill_zero(void *p, size_t bytes, int first)
-{
-    const size_t n16 = (((uintptr_t)p & 15) == 0) ? bytes / 16 : 0;
-    const size_t t = (size_t)(blockIdx.x - first) * blockDim.x + threadIdx.x;
-    const size_t n = (size_t)(gridDim.x - first) * blockDim.x;
-    for (size_t i = t; i < n16; i += n) ((uint4 *)p)[i] = make_uint4(0, 0, 0, 0);
-    for (size_t i = n16 * 16 + t * 2; i + 1 < bytes; i += n * 2) *(uint16_t *)((char *)p + i) = 0;
-}
+// Ids that do not occur get rows of zeros.  The table's first rows are
+// written beside the sort, whoever they belong to, as many as the idle SMs
+// manage meanwhile; the rest beside the sums, by blocks that skip the rows
+// whose bit says that the token occurs (8192 rows of 4096, vocabulary 151936:
+// all zeros beside the sort, then the sums, 294 us; like this 243 us, of
+// a floor of 204 us).
+struct ZeroFill {
+    char *p;              // the table, or null (accumulating)
+    size_t begin, end;    // bytes that this launch writes; the sums' launch: from begin on
+    unsigned *bits;       // one bit per id, or null: everything is written beside the sort
+    int words;
+};
 
 constexpr int kSortThreads = 1024;
+// the one-block sort takes about 5 us for every 1024 rows, 6 TB/s meanwhile is
+// this much a row; a launch of the radix sort about 10 us
+constexpr size_t kZeroPerRow = (size_t)32 << 10, kZeroPerLaunch = (size_t)64 << 20;
 
-// Up to kSortSmall rows: block 0 sorts (token, row) pairs in shared memory
-// (bitonic network: comparisons fixed by the size alone), the other blocks
-// write the zeros meanwhile.
-template <class K>
-__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const int32_t *ids, int rows, int vocab, int row_bits,
-                                                                  int32_t *tok, int32_t *idx, void *zero,
-                                                                  size_t zero_bytes, unsigned *err)
+__device__ __forceinline__ void fill_zero(const ZeroFill &z, int first_block)
 {
-    extern __shared__ __align__(16) unsigned char sort_smem[];
-    K *key = (K *)sort_smem;
+    zero_span(z.p + z.begin, z.end - z.begin, (size_t)(blockIdx.x - first_block) * blockDim.x + threadIdx.x,
+              (size_t)(gridDim.x - first_block) * blockDim.x);
+}
+
+// Bitonic network over kSortThreads * E keys, thread t holding keys t E ..
+// t E + E - 1: exchanges within a thread stay in registers, within a warp go
+// through shuffles, the others through shared memory.
+template <class K, int E> constexpr int kSortHold = E * sizeof(K) > 32 ? 32 / sizeof(K) : E;   // keys of a thread in smem
+
+template <class K, int E> __device__ __forceinline__ void bitonic_sort(K (&key)[E], int n, K *sm)
+{
+    const int t = threadIdx.x;
+    for (int k = 2; k <= n; k <<= 1) {
+        for (int j = k >> 1; j >= E; j >>= 1) {
+            const int tj = j / E;
+            K other[E];
+            if (tj >= 32) {
+                constexpr int H = kSortHold<K, E>;
+#pragma unroll
+                for (int h = 0; h < E; h += H) {
+                    __syncthreads();
+#pragma unroll
+                    for (int e = 0; e < H; ++e) sm[e * kSortThreads + t] = key[h + e];
+                    __syncthreads();
+#pragma unroll
+                    for (int e = 0; e < H; ++e) other[h + e] = sm[e * kSortThreads + (t ^ tj)];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) other[e] = __shfl_xor_sync(0xffffffffu, key[e], tj);
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const bool up = ((t * E + e) & k) == 0, low = (t & tj) == 0;
+                if ((key[e] > other[e]) == (up == low)) key[e] = other[e];
+            }
+        }
+#pragma unroll
+        for (int j = E / 2; j > 0; j >>= 1)
+            if (j < k)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    if (e & j) continue;
+                    const bool up = ((t * E + e) & k) == 0;
+                    const K a = key[e], b = key[e + j];
+                    if ((a > b) == up) { key[e] = b; key[e + j] = a; }
+                }
+    }
+}
+
+// Up to kSortSmall rows: block 0 sorts (token, row) pairs, the other blocks
+// write the first zeros meanwhile.
+template <class K, int E>
+__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const int32_t *ids, int rows, int vocab, int row_bits,
+                                                                  int32_t *tok, int32_t *idx, ZeroFill z, unsigned *err)
+{
+    __shared__ K sm[kSortThreads * kSortHold<K, E>];
+    __shared__ int32_t last[kSortThreads];
     pdl_trigger();
     pdl_wait();
     if (blockIdx.x > 0) {
-        fill_zero(zero, zero_bytes, 1);
+        fill_zero(z, 1);
         return;
     }
+    if (z.bits)
+        for (int i = threadIdx.x; i < z.words; i += kSortThreads) z.bits[i] = 0;
     int n = 2;
     while (n < rows) n <<= 1;
-    for (int i = threadIdx.x; i < n; i += kSortThreads)
-        key[i] = i < rows ? (((K)sort_key(ids, i, vocab, err) << row_bits) | (K)i) : ~(K)0;
-    for (int k = 2; k <= n; k <<= 1)
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            __syncthreads();
-            for (int p = threadIdx.x; p < n / 2; p += kSortThreads) {
-                const int lo = 2 * p - (p & (j - 1)), hi = lo + j;   // pair p of distance j
-                const K a = key[lo], b = key[hi];
-                if ((a > b) == ((lo & k) == 0)) { key[lo] = b; key[hi] = a; }
-            }
-        }
+    K key[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = threadIdx.x * E + e;
+        key[e] = i < rows ? (((K)sort_key(ids, i, vocab, err) << row_bits) | (K)i) : ~(K)0;
+    }
+    bitonic_sort<K, E>(key, n, sm);
+    last[threadIdx.x] = (int32_t)(key[E - 1] >> row_bits);
     __syncthreads();
-    for (int i = threadIdx.x; i < rows; i += kSortThreads) {
-        tok[i] = (int32_t)(key[i] >> row_bits);
-        idx[i] = (int32_t)(key[i] & (((K)1 << row_bits) - 1));
+    int prev = threadIdx.x ? last[threadIdx.x - 1] : -1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int i = threadIdx.x * E + e;
+        if (i >= rows) break;
+        const int t = (int32_t)(key[e] >> row_bits);
+        tok[i] = t;
+        idx[i] = (int32_t)(key[e] & (((K)1 << row_bits) - 1));
+        if (z.bits && t != prev && t < vocab) atomicOr(&z.bits[t >> 5], 1u << (t & 31));
+        prev = t;
     }
 }
 
@@ -213,14 +286,18 @@ constexpr int kRadixThreads = 256, kRadixWarps = kRadixThreads / 32, kRadixPer =
 
 template <bool FIRST>
 __global__ void __launch_bounds__(kRadixThreads) radix_hist_kernel(const int32_t *src, int rows, int vocab, int tiles,
-                                                                   int shift, int bits, int *hist, void *zero,
-                                                                   size_t zero_bytes, unsigned *err)
+                                                                   int shift, int bits, int *hist, ZeroFill z,
+                                                                   unsigned *err)
 {
     __shared__ int h[1 << kSortDigit];
     pdl_trigger();
     pdl_wait();
     if ((int)blockIdx.x >= tiles) {
-        fill_zero(zero, zero_bytes, tiles);
+        if (FIRST && z.bits)
+            for (int i = (blockIdx.x - tiles) * kRadixThreads + threadIdx.x; i < z.words;
+                 i += (gridDim.x - tiles) * kRadixThreads)
+                z.bits[i] = 0;
+        fill_zero(z, tiles);
         return;
     }
     for (int i = threadIdx.x; i < (1 << bits); i += kRadixThreads) h[i] = 0;
@@ -288,11 +365,16 @@ __global__ void __launch_bounds__(1024) radix_scan_kernel(int *h, int n)
 template <bool FIRST>
 __global__ void __launch_bounds__(kRadixThreads) radix_scatter_kernel(const int32_t *src_tok, const int32_t *src_idx,
                                                                       int rows, int vocab, int tiles, int shift, int bits,
-                                                                      const int *hist, int32_t *tok, int32_t *idx)
+                                                                      const int *hist, int32_t *tok, int32_t *idx,
+                                                                      ZeroFill z)
 {
     __shared__ int cnt[kRadixWarps][1 << kSortDigit];
     pdl_trigger();
     pdl_wait();
+    if ((int)blockIdx.x >= tiles) {
+        fill_zero(z, tiles);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nb = 1 << bits;
     for (int i = threadIdx.x; i < kRadixWarps * nb; i += kRadixThreads) cnt[i / nb][i % nb] = 0;
     __syncthreads();
@@ -328,6 +410,11 @@ __global__ void __launch_bounds__(kRadixThreads) radix_scatter_kernel(const int3
     for (int j = 0; j < kRadixPer; ++j) {
         const int i = base + j * 32 + lane;
         if (i >= rows) continue;
+        if (FIRST && z.bits && key[j] < vocab) {
+            unsigned *w = &z.bits[key[j] >> 5];
+            const unsigned b = 1u << (key[j] & 31);
+            if (!(*(volatile unsigned *)w & b)) atomicOr(w, b);   // (few atomics where most rows share a token)
+        }
         const int pos = cnt[warp][(key[j] >> shift) & (nb - 1)] + rank[j];
         tok[pos] = key[j];
         idx[pos] = FIRST ? i : src_idx[i];
@@ -335,12 +422,14 @@ __global__ void __launch_bounds__(kRadixThreads) radix_scatter_kernel(const int3
 }
 
 // One block per (piece, column slab): runs of equal tokens summed in fp32.
+// Blocks from run_blocks on write the remaining zeros, a warp per absent row.
 constexpr int kRunThreads = 128;
 
 template <class T, class TG, int VEC>
 __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const T *dout, const int32_t *tok, const int32_t *idx,
-                                                              int rows, int d, int vocab, int P, float scale,
-                                                              int accumulate, TG *dtable, float *part)
+                                                              int rows, int d, int vocab, int P, int slabs,
+                                                              int run_blocks, float scale, int accumulate, TG *dtable,
+                                                              float *part, ZeroFill z)
 {
     constexpr int J = VEC == 8 ? 1 : 4;      // column chunks of a thread
     constexpr int U = VEC == 8 ? 8 : 4;      // rows in flight
@@ -348,11 +437,20 @@ __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const T *dout, con
     int *st = run_smem, *si = run_smem + P;
     pdl_trigger();
     pdl_wait();
-    const int lo = blockIdx.x * P, hi = min(rows, lo + P), n = hi - lo;
+    if ((int)blockIdx.x >= run_blocks) {
+        const size_t row_bytes = (size_t)d * sizeof(TG);
+        const int warps = (gridDim.x - run_blocks) * (kRunThreads / 32);
+        for (int v = (int)(z.begin / row_bytes) + (blockIdx.x - run_blocks) * (kRunThreads / 32) + (threadIdx.x >> 5);
+             v < vocab; v += warps)
+            if (!(z.bits[v >> 5] >> (v & 31) & 1)) zero_span(z.p + (size_t)v * row_bytes, row_bytes, threadIdx.x & 31, 32);
+        return;
+    }
+    const int piece = blockIdx.x / slabs;
+    const int lo = piece * P, hi = min(rows, lo + P), n = hi - lo;
     for (int i = threadIdx.x; i < n; i += kRunThreads) { st[i] = tok[lo + i]; si[i] = idx[lo + i]; }
     const int prev = lo > 0 ? tok[lo - 1] : -1, next = hi < rows ? tok[hi] : -1;
     __syncthreads();
-    const int c0 = blockIdx.y * kRunThreads * J;
+    const int c0 = (blockIdx.x % slabs) * kRunThreads * J;
     float acc[J][VEC];
     auto clear = [&]() {
 #pragma unroll
@@ -368,7 +466,7 @@ __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const T *dout, con
             const int c = (c0 + j * kRunThreads + threadIdx.x) * VEC;
             if (c >= d) continue;
             if (head || tail) {
-                float *p = part + ((size_t)blockIdx.x * 2 + (head ? 0 : 1)) * d + c;
+                float *p = part + ((size_t)piece * 2 + (head ? 0 : 1)) * d + c;
 #pragma unroll
                 for (int q = 0; q < VEC; ++q) p[q] = acc[j][q];
             } else {
@@ -416,81 +514,143 @@ __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const T *dout, con
 }
 
 // Runs that cross pieces: the piece a run starts in adds up its partials in
-// order.  32 columns x 8 strands of pieces per block; the strands join in
-// order too.
-constexpr int kJoinCols = 32, kJoinStrands = 8;
+// order.  A block looks at up to 32 pieces (blockIdx.x, + gridDim.x, ..) for
+// runs that start there; 32 threads of VEC columns x 8 strands of pieces add
+// up, and the strands join in order too.
+constexpr int kJoinLanes = 32, kJoinStrands = 8, kJoinThreads = kJoinLanes * kJoinStrands;
+constexpr int kJoinBlocks = 64;
 
-template <class TG>
-__global__ void __launch_bounds__(kJoinCols *kJoinStrands) run_join_kernel(const int32_t *tok, int rows, int d, int vocab,
-                                                                           int P, float scale, int accumulate, TG *dtable,
-                                                                           const float *part)
+template <class TG, int VEC>
+__global__ void __launch_bounds__(kJoinThreads) run_join_kernel(const int32_t *tok, int rows, int d, int vocab, int pieces,
+                                                                int P, float scale, int accumulate, TG *dtable,
+                                                                const float *part)
 {
-    __shared__ float red[kJoinStrands][kJoinCols];
+    __shared__ float red[kJoinStrands][kJoinLanes * VEC];
+    __shared__ unsigned starts;
     pdl_trigger();
     pdl_wait();
-    const int piece = blockIdx.x, lo = piece * P, hi = min(rows, lo + P);
-    if (hi >= rows) return;
-    const int cur = tok[hi - 1];
-    if (tok[hi] != cur || cur >= vocab) return;              // no run leaves this piece
-    if (lo > 0 && tok[lo] == cur && tok[lo - 1] == cur) return;   // it started earlier
-    const int x = threadIdx.x % kJoinCols, y = threadIdx.x / kJoinCols, c = blockIdx.y * kJoinCols + x;
-    float sum = 0.f;
-    if (c < d) {
-        if (y == 0) sum = part[((size_t)piece * 2 + 1) * d + c];
-#pragma unroll 4
-        for (int q = piece + 1 + y; (size_t)q * P < (size_t)rows && tok[(size_t)q * P] == cur; q += kJoinStrands)
-            sum += part[(size_t)q * 2 * d + c];
+    const int x = threadIdx.x % kJoinLanes, y = threadIdx.x / kJoinLanes;
+    if (y == 0) {
+        const int q = blockIdx.x + x * gridDim.x, lo = q * P, hi = lo + P;
+        bool s = false;
+        if (q < pieces - 1) {   // (the last piece has no successor)
+            const int a = tok[hi - 1], b = tok[hi], c = tok[lo], e = lo > 0 ? tok[lo - 1] : -1;
+            s = a == b && a < vocab && !(c == a && e == a);   // leaves the piece, and did not enter it
+        }
+        const unsigned m = __ballot_sync(0xffffffffu, s);
+        if (x == 0) starts = m;
     }
-    red[y][x] = sum;
     __syncthreads();
-    if (y == 0 && c < d) {
-        float t = red[0][x];
+    const int c = (blockIdx.y * kJoinLanes + x) * VEC;
+    for (unsigned m = starts; m; m &= m - 1) {
+        const int piece = blockIdx.x + (__ffs(m) - 1) * gridDim.x, cur = tok[(piece + 1) * P];
+        int n = 0;   // pieces after this one that begin with the run
+        for (int q0 = piece + 1;; q0 += kJoinThreads) {
+            const int q = q0 + threadIdx.x;
+            const int k = __syncthreads_count(q < pieces && tok[q * P] == cur);
+            n += k;
+            if (k < kJoinThreads) break;
+        }
+        float sum[VEC];
 #pragma unroll
-        for (int k = 1; k < kJoinStrands; ++k) t += red[k][x];
-        TG *o = dtable + (size_t)cur * d + c;
-        *o = from_f<TG>(accumulate ? fmaf(scale, t, to_f<TG>(*o)) : scale * t);
+        for (int e = 0; e < VEC; ++e) sum[e] = 0.f;
+        if (c < d) {
+            const float *p = part + (size_t)piece * 2 * d + c;
+            auto add = [&](const float *f) {
+                if constexpr (VEC == 4) {
+                    const float4 v = *(const float4 *)f;
+                    sum[0] += v.x; sum[1] += v.y; sum[2] += v.z; sum[3] += v.w;
+                } else {
+                    sum[0] += *f;
+                }
+            };
+            if (y == 0) add(p + d);
+#pragma unroll 8
+            for (int q = 1 + y; q <= n; q += kJoinStrands) add(p + (size_t)q * 2 * d);
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) red[y][x * VEC + e] = sum[e];
+        __syncthreads();
+        for (int i = threadIdx.x; i < kJoinLanes * VEC; i += kJoinThreads) {
+            const int col = blockIdx.y * kJoinLanes * VEC + i;
+            if (col >= d) continue;
+            float t = red[0][i];
+#pragma unroll
+            for (int k = 1; k < kJoinStrands; ++k) t += red[k][i];
+            TG *o = dtable + (size_t)cur * d + col;
+            *o = from_f<TG>(accumulate ? fmaf(scale, t, to_f<TG>(*o)) : scale * t);
+        }
+        __syncthreads();
     }
 }
 
-__global__ void __launch_bounds__(kSortThreads) fill_zero_kernel(void *p, size_t bytes)
+__global__ void __launch_bounds__(kSortThreads) fill_zero_kernel(ZeroFill z)
 {
     pdl_trigger();
     pdl_wait();
-    fill_zero(p, bytes, 0);
+    fill_zero(z, 0);
 }
 
 template <class T, class TG>
 static cudaError_t run_sums(const EmbedGradArgs &a, const EmbedGradPlan &p, const int32_t *tok, const int32_t *idx,
-                            cudaStream_t s)
+                            const ZeroFill &z, cudaStream_t s)
 {
     float *part = (float *)(a.ws + p.o_part);
     const bool vec = rows_aligned(a.dout, a.d) && rows_aligned(a.dtable, a.d);
-    const int cols = vec ? 8 * kRunThreads : 4 * kRunThreads;
-    const dim3 grid(p.pieces, (a.d + cols - 1) / cols);
-    cudaError_t e;
-    if (vec)
-        e = launch_k(run_sum_kernel<T, TG, 8>, grid, kRunThreads, (size_t)p.piece * 8, s, (const T *)a.dout, tok, idx,
-                     a.rows, a.d, a.vocab, p.piece, a.scale, a.accumulate, (TG *)a.dtable, part);
-    else
-        e = launch_k(run_sum_kernel<T, TG, 1>, grid, kRunThreads, (size_t)p.piece * 8, s, (const T *)a.dout, tok, idx,
-                     a.rows, a.d, a.vocab, p.piece, a.scale, a.accumulate, (TG *)a.dtable, part);
+    const int cols = vec ? 8 * kRunThreads : 4 * kRunThreads, slabs = (a.d + cols - 1) / cols;
+    const int run_blocks = p.pieces * slabs, fill_blocks = z.bits && z.begin < (size_t)a.vocab * a.d * sizeof(TG) ? 8 * 148 : 0;
+    auto sum = [&](auto kernel) {
+        return launch_k(kernel, run_blocks + fill_blocks, kRunThreads, (size_t)p.piece * 8, s, (const T *)a.dout, tok, idx,
+                        a.rows, a.d, a.vocab, p.piece, slabs, run_blocks, a.scale, a.accumulate, (TG *)a.dtable, part, z);
+    };
+    cudaError_t e = vec ? sum(run_sum_kernel<T, TG, 8>) : sum(run_sum_kernel<T, TG, 1>);
     if (e != cudaSuccess || p.pieces < 2) return e;
-    return launch_k(run_join_kernel<TG>, dim3(p.pieces - 1, (a.d + kJoinCols - 1) / kJoinCols), kJoinCols * kJoinStrands,
-                    0, s, tok, a.rows, a.d, a.vocab, p.piece, a.scale, a.accumulate, (TG *)a.dtable, (const float *)part);
+    auto join = [&](auto kernel, int per) {
+        return launch_k(kernel, dim3(std::min(kJoinBlocks, p.pieces - 1), (a.d + per - 1) / per), kJoinThreads, 0, s, tok,
+                        a.rows, a.d, a.vocab, p.pieces, p.piece, a.scale, a.accumulate, (TG *)a.dtable, (const float *)part);
+    };
+    return a.d % 4 == 0 ? join(run_join_kernel<TG, 4>, kJoinLanes * 4) : join(run_join_kernel<TG, 1>, kJoinLanes);
+}
+
+template <class K>
+static cudaError_t sort_small(const EmbedGradArgs &a, int row_bits, int32_t *tok, int32_t *idx, const ZeroFill &z, int fill,
+                              cudaStream_t s)
+{
+    auto go = [&](auto kernel) {
+        return launch_k(kernel, 1 + fill, kSortThreads, 0, s, a.ids, a.rows, a.vocab, row_bits, tok, idx, z, a.err);
+    };
+    // keys per thread: as few as hold the rows
+    return a.rows <= kSortThreads ? go(sort_small_kernel<K, 1>)
+           : a.rows <= 2 * kSortThreads ? go(sort_small_kernel<K, 2>)
+           : a.rows <= 4 * kSortThreads ? go(sort_small_kernel<K, 4>)
+                                        : go(sort_small_kernel<K, 8>);
 }
 
 cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t s)
 {
-    const size_t bytes = (size_t)a.vocab * a.d * (a.dtable_dtype == ORTHRUS_BF16 ? 2 : 4);
-    const size_t zero_bytes = a.accumulate ? 0 : bytes;
-    // blocks that write zeros: two of 1024 threads per SM, fewer for small tables
-    const int fill = zero_bytes ? (int)std::min<size_t>(2 * 148, (zero_bytes + 16383) / 16384) : 0;
+    const size_t row_bytes = (size_t)a.d * (a.dtable_dtype == ORTHRUS_BF16 ? 2 : 4), bytes = (size_t)a.vocab * row_bytes;
+    ZeroFill z{};
+    if (!a.accumulate) z.p = (char *)a.dtable;
+    // the next `most` bytes of zeros (whole rows) go to the next launch; its
+    // blocks for them: two of 1024 threads per SM, fewer for few bytes
+    auto share = [&](size_t most) {
+        z.begin = z.end;
+        if (!z.p) return 0;
+        z.end = bytes - z.begin <= most ? bytes : z.begin + most / row_bytes * row_bytes;
+        return (int)std::min<size_t>(2 * 148, (z.end - z.begin + 16383) / 16384);
+    };
     cudaError_t e;
     if (a.rows == 0) {
-        if (!fill) return cudaSuccess;
-        return launch_k(fill_zero_kernel, fill, kSortThreads, 0, s, a.dtable, zero_bytes);
+        const int fill = share(bytes);
+        return fill ? launch_k(fill_zero_kernel, fill, kSortThreads, 0, s, z) : cudaSuccess;
     }
     const EmbedGradPlan p = plan_embed_grad(a.rows, a.vocab, a.d);
+    const size_t beside = a.rows <= kSortSmall ? std::max(a.rows, 1024) * kZeroPerRow
+                                               : 2 * p.digits * (kZeroPerLaunch / row_bytes * row_bytes);
+    if (z.p && bytes > beside) {
+        z.bits = (unsigned *)(a.ws + p.o_bits);
+        z.words = (a.vocab + 31) / 32;
+    }
     int32_t *tok[2] = {(int32_t *)(a.ws + p.o_tok[0]), (int32_t *)(a.ws + p.o_tok[1])};
     int32_t *idx[2] = {(int32_t *)(a.ws + p.o_idx[0]), (int32_t *)(a.ws + p.o_idx[1])};
     int cur = 0;
@@ -499,48 +659,46 @@ cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t s)
         while (n < a.rows) { n <<= 1; ++row_bits; }
         int key_bits = 1;
         while (key_bits < 31 && (a.vocab >> key_bits) != 0) ++key_bits;
+        const int fill = share(beside);
         // 32-bit keys while (token, row) fits below the padding key
-        if (key_bits + row_bits <= 31)
-            e = launch_k(sort_small_kernel<uint32_t>, 1 + fill, kSortThreads, (size_t)n * 4, s, a.ids, a.rows, a.vocab,
-                         row_bits, tok[0], idx[0], a.dtable, zero_bytes, a.err);
-        else {
-            e = cudaFuncSetAttribute(sort_small_kernel<uint64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     kSortSmall * 8);
-            if (e != cudaSuccess) return e;
-            e = launch_k(sort_small_kernel<uint64_t>, 1 + fill, kSortThreads, (size_t)n * 8, s, a.ids, a.rows, a.vocab,
-                         row_bits, tok[0], idx[0], a.dtable, zero_bytes, a.err);
-        }
+        e = key_bits + row_bits <= 31 ? sort_small<uint32_t>(a, row_bits, tok[0], idx[0], z, fill, s)
+                                      : sort_small<uint64_t>(a, row_bits, tok[0], idx[0], z, fill, s);
         if (e != cudaSuccess) return e;
     } else {
         int *hist = (int *)(a.ws + p.o_hist);
         const int32_t *st = a.ids, *si = nullptr;
         for (int pass = 0; pass < p.digits; ++pass) {
             const int shift = pass * p.digit_bits;
+            int fill = 4 * share(kZeroPerLaunch);   // (these blocks are a quarter as large)
             if (pass == 0)
-                e = launch_k(radix_hist_kernel<true>, p.tiles + 4 * fill, kRadixThreads, 0, s, st, a.rows, a.vocab,
-                             p.tiles, shift, p.digit_bits, hist, a.dtable, zero_bytes, a.err);
+                e = launch_k(radix_hist_kernel<true>, p.tiles + fill, kRadixThreads, 0, s, st, a.rows, a.vocab, p.tiles,
+                             shift, p.digit_bits, hist, z, a.err);
             else
-                e = launch_k(radix_hist_kernel<false>, p.tiles, kRadixThreads, 0, s, st, a.rows, a.vocab, p.tiles, shift,
-                             p.digit_bits, hist, a.dtable, (size_t)0, a.err);
+                e = launch_k(radix_hist_kernel<false>, p.tiles + fill, kRadixThreads, 0, s, st, a.rows, a.vocab, p.tiles,
+                             shift, p.digit_bits, hist, z, a.err);
             if (e != cudaSuccess) return e;
             e = launch_k(radix_scan_kernel, 1, 1024, 0, s, hist, p.tiles << p.digit_bits);
             if (e != cudaSuccess) return e;
+            fill = 4 * share(kZeroPerLaunch);
             if (pass == 0)
-                e = launch_k(radix_scatter_kernel<true>, p.tiles, kRadixThreads, 0, s, st, si, a.rows, a.vocab, p.tiles,
-                             shift, p.digit_bits, (const int *)hist, tok[0], idx[0]);
+                e = launch_k(radix_scatter_kernel<true>, p.tiles + fill, kRadixThreads, 0, s, st, si, a.rows, a.vocab,
+                             p.tiles, shift, p.digit_bits, (const int *)hist, tok[0], idx[0], z);
             else
-                e = launch_k(radix_scatter_kernel<false>, p.tiles, kRadixThreads, 0, s, st, si, a.rows, a.vocab, p.tiles,
-                             shift, p.digit_bits, (const int *)hist, tok[pass & 1], idx[pass & 1]);
+                e = launch_k(radix_scatter_kernel<false>, p.tiles + fill, kRadixThreads, 0, s, st, si, a.rows, a.vocab,
+                             p.tiles, shift, p.digit_bits, (const int *)hist, tok[pass & 1], idx[pass & 1], z);
             if (e != cudaSuccess) return e;
             cur = pass & 1;
             st = tok[cur];
             si = idx[cur];
         }
     }
+    z.begin = z.end;
     const bool ib = a.dout_dtype == ORTHRUS_BF16, ob = a.dtable_dtype == ORTHRUS_BF16;
     if (ib)
-        return ob ? run_sums<bf16, bf16>(a, p, tok[cur], idx[cur], s) : run_sums<bf16, float>(a, p, tok[cur], idx[cur], s);
-    return ob ? run_sums<float, bf16>(a, p, tok[cur], idx[cur], s) : run_sums<float, float>(a, p, tok[cur], idx[cur], s);
+        return ob ? run_sums<bf16, bf16>(a, p, tok[cur], idx[cur], z, s)
+                  : run_sums<bf16, float>(a, p, tok[cur], idx[cur], z, s);
+    return ob ? run_sums<float, bf16>(a, p, tok[cur], idx[cur], z, s)
+              : run_sums<float, float>(a, p, tok[cur], idx[cur], z, s);
 }
 
 // ---------------------------------------------------------------- RMSNorm

@@ -150,6 +150,38 @@ def test_embed_grad_huge_vocabulary_keys():
     within(got, want, half(F32) * want.abs() + (cnt[:, None] + 3) * U * mag)
 
 
+@pytest.mark.parametrize("n", [1023, 1025, 2048, 3000, 4096, 5000])
+@pytest.mark.parametrize("V", [50, 3999999])
+def test_embed_grad_one_block_sort(n, V):
+    """Every number of keys per thread, 32- and 64-bit keys."""
+    d = 3
+    dout, ids = _embed_grad_case(n, d, V, F32, "padded")
+    got = pkg.orthrus_embed_grad(dout, ids, V)
+    want, mag, cnt = _embed_grad_want(dout, ids, V, 1.0)
+    within(got, want, half(F32) * want.abs() + (cnt[:, None] + 3) * U * mag)
+
+
+@pytest.mark.parametrize("n,d,V,dt,odt,kind", [
+    (300, 1000, 40000, BF, BF, "any"), (9000, 129, 151936, BF, F32, "blocks"), (2500, 33, 1100000, F32, BF, "padded"),
+    (5, 4096, 9000, BF, BF, "one"), (9000, 1000, 134217, BF, BF, "any"), (9000, 1500, 151936, BF, BF, "blocks"), (70000, 8, 2200000, BF, F32, "any"), (3, 65536, 600, F32, BF, "any")])
+def test_embed_grad_large_tables(n, d, V, dt, odt, kind):
+    """Tables whose zeros are written beside the sums, whatever they held."""
+    dout, ids = _embed_grad_case(n, d, V, dt, kind)
+    ids[0] = 0
+    ids[-1] = V - 1
+    want, mag, cnt = _embed_grad_want(dout, ids, V, 1.0)
+    tol = half(odt) * want.abs() + (cnt[:, None] + 3) * U * mag
+    del mag
+    for out in (torch.full((V, d), float("nan"), dtype=odt, device=DEV),
+                misaligned(torch.full((V, d), float("nan"), dtype=odt, device=DEV))):
+        got = pkg.orthrus_embed_grad(dout, ids, V, out=out)
+        within(got, want, tol)
+        assert torch.count_nonzero(got[cnt == 0]) == 0
+    base = torch.ones((V, d), dtype=odt, device=DEV)
+    pkg.orthrus_embed_grad(dout, ids, V, out=base, accumulate=True)
+    assert bool((base[cnt == 0] == 1).all())
+
+
 @pytest.mark.parametrize("n,V", [(100, 64), (9000, 64)])
 def test_embed_grad_accumulates(n, V):
     d = 48
@@ -664,5 +696,8 @@ def test_binding_refusals_on_device():
         pkg.orthrus_embed_rows(w.half(), t)
     with pytest.raises(ValueError):
         pkg.orthrus_embed_grad(h, t, 100, accumulate=True)
+    for vocab in (0, -1, (1 << 32) + 100):
+        with pytest.raises(ValueError):
+            pkg.orthrus_embed_grad(h, t, vocab)
     with pytest.raises(pkg.OrthrusError):
         pkg.orthrus_rmsnorm(h, torch.ones(64, device=DEV), EPS)       # bf16 rows, fp32 gain
