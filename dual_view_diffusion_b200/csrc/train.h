@@ -96,7 +96,6 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s);
 cudaError_t launch_ce_finalize(const float2 *rec, const float *zt, const LossArgs &a, int n_tiles, int exact,
                                cudaStream_t s);
 cudaError_t launch_part_sum(const float *part, int splits, size_t n, void *out, int dtype, cudaStream_t s);
-cudaError_t launch_clean_rows(const LossArgs &a, void *out, cudaStream_t s);
 cudaError_t launch_loss_fwd(const LossArgs &a, cudaStream_t s);
 cudaError_t launch_loss_grad(const LossArgs &a, cudaStream_t s);
 

@@ -25,16 +25,22 @@ namespace orthrus {
 
 // ---------------------------------------------------------------- tiles
 constexpr int kSt = 64;            // rows and columns of a SIMT tile
-constexpr int kStK = 16;           // k per step
+constexpr int kStK = 32;           // k per step
 constexpr int kStThreads = 256;
-constexpr int kStFlush = 8;        // steps per partial sum (128 products)
+constexpr int kStFlush = 4;        // steps per partial sum (128 products)
+constexpr int kStLoads = kSt * kStK / kStThreads;
 
-// A strided operand: element (row, k).
+// A strided operand: element (row, k).  With `live`, a k whose byte is zero
+// reads as zeros whatever it holds.
 template <class T> struct Operand {
     const T *p;
     size_t row_stride, k_stride;
     int rows;
-    __device__ __forceinline__ float at(int r, size_t k) const { return to_f<T>(p[r * row_stride + k * k_stride]); }
+    const unsigned char *live;
+    __device__ __forceinline__ float at(int r, size_t k) const
+    {
+        return live && !live[k] ? 0.f : to_f<T>(p[r * row_stride + k * k_stride]);
+    }
 };
 
 // acc[i][j] = sum over k in [k0, k1) of A(m0 + 4 ty + i, k) B(n0 + 4 tx + j, k).
@@ -50,10 +56,10 @@ __device__ void simt_tile(const Operand<TA> &A, const Operand<TB> &B, int m0, in
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) { acc[i][j] = 0.f; part[i][j] = 0.f; }
-    float ra[4], rb[4];
+    float ra[kStLoads], rb[kStLoads];
     auto fetch = [&](size_t k) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {   // consecutive threads walk the contiguous axis
+        for (int q = 0; q < kStLoads; ++q) {   // consecutive threads walk the contiguous axis
             const int e = threadIdx.x + q * kStThreads;
             const int ar = AK ? e / kStK : e % kSt, ak = AK ? e % kStK : e / kSt;
             const int br = BK ? e / kStK : e % kSt, bk = BK ? e % kStK : e / kSt;
@@ -65,7 +71,7 @@ __device__ void simt_tile(const Operand<TA> &A, const Operand<TB> &B, int m0, in
     int step = 0;
     for (size_t k = k0; k < k1; k += kStK) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < kStLoads; ++q) {
             const int e = threadIdx.x + q * kStThreads;
             if (AK) sa[e % kStK][e / kStK] = ra[q]; else sa[e / kSt][e % kSt] = ra[q];
             if (BK) sb[e % kStK][e / kStK] = rb[q]; else sb[e / kSt][e % kSt] = rb[q];
@@ -110,7 +116,7 @@ __global__ void __launch_bounds__(kStThreads) ce_tile_simt(const T *h, const T *
     pdl_wait();
     const int m0 = blockIdx.y * kSt, n0 = blockIdx.x * kSt;
     float acc[4][4];
-    const Operand<T> A{h, (size_t)d, 1, N}, B{w, (size_t)d, 1, V};
+    const Operand<T> A{h, (size_t)d, 1, N, nullptr}, B{w, (size_t)d, 1, V, nullptr};
     simt_tile<T, T, true, true>(A, B, m0, n0, 0, d, acc, sm.a, sm.b);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
@@ -231,7 +237,7 @@ cudaError_t launch_ce_finalize(const float2 *rec, const float *zt, const LossArg
 // upstream gradient is zero, or that has no target, gets exact zeros
 // whatever its hidden row holds.
 template <class T, bool KL>
-__global__ void __launch_bounds__(kStThreads) dz_tile_simt(LossArgs a, int v0, int Vp, float *dz)
+__global__ void __launch_bounds__(kStThreads) dz_tile_simt(LossArgs a, int v0, int Vp, float *dz, unsigned char *alive)
 {
     __shared__ __align__(16) StSmem sm;
     pdl_trigger();
@@ -239,10 +245,10 @@ __global__ void __launch_bounds__(kStThreads) dz_tile_simt(LossArgs a, int v0, i
     const int m0 = blockIdx.y * kSt, n0 = v0 + blockIdx.x * kSt, d = a.d;
     const int vend = min(a.V, v0 + Vp);
     float z[4][4], z2[4][4];
-    const Operand<T> A{(const T *)a.h, (size_t)d, 1, a.N}, B{(const T *)a.w, (size_t)d, 1, a.V};
+    const Operand<T> A{(const T *)a.h, (size_t)d, 1, a.N, nullptr}, B{(const T *)a.w, (size_t)d, 1, a.V, nullptr};
     simt_tile<T, T, true, true>(A, B, m0, n0, 0, d, z, sm.a, sm.b);
     if (KL) {
-        const Operand<T> A2{(const T *)a.h2, (size_t)d, 1, a.N};
+        const Operand<T> A2{(const T *)a.h2, (size_t)d, 1, a.N, nullptr};
         simt_tile<T, T, true, true>(A2, B, m0, n0, 0, d, z2, sm.a, sm.b);
     }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -258,6 +264,7 @@ __global__ void __launch_bounds__(kStThreads) dz_tile_simt(LossArgs a, int v0, i
             t = a.targets[row];
             if (t >= a.V && tx == 0 && blockIdx.x == 0 && a.err) raise_err(a.err, ORTHRUS_DEVERR_TOKEN);
             if (t < 0 || t >= a.V) g = 0.f;
+            if (alive && v0 == 0 && blockIdx.x == 0 && tx == 0) alive[row] = g != 0.f;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -280,12 +287,11 @@ struct GradGemm {
     void *out;
 };
 template <class TA, class TB, bool AK, class TO>
-__global__ void __launch_bounds__(kStThreads) grad_gemm_simt(Operand<TA> A, Operand<TB> B, GradGemm g)
+__device__ __forceinline__ void grad_tile(const Operand<TA> &A, const Operand<TB> &B, const GradGemm &g, unsigned block,
+                                          StSmem &sm)
 {
-    __shared__ __align__(16) StSmem sm;
-    pdl_trigger();
-    pdl_wait();
-    const int m0 = blockIdx.y * kSt, n0 = blockIdx.x * kSt, sp = blockIdx.z;
+    const unsigned nt = (g.N + kSt - 1) / kSt, mt = (g.M + kSt - 1) / kSt;
+    const int n0 = block % nt * kSt, m0 = block / nt % mt * kSt, sp = block / nt / mt;
     const size_t per = (((size_t)g.K + g.splits - 1) / g.splits + kStK - 1) / kStK * kStK;
     const size_t k0 = min((size_t)g.K, per * sp), k1 = min((size_t)g.K, k0 + per);
     float acc[4][4];
@@ -310,6 +316,19 @@ __global__ void __launch_bounds__(kStThreads) grad_gemm_simt(Operand<TA> A, Oper
     }
 }
 
+// Both products of a piece's dz in one launch (neither fills the GPU at the
+// sizes this path serves): blocks below h_blocks make dh, the others dW.
+template <class T>
+__global__ void __launch_bounds__(kStThreads) grads_simt(Operand<float> dz, Operand<T> w, GradGemm gh, unsigned h_blocks,
+                                                         Operand<float> dzt, Operand<T> h, GradGemm gw)
+{
+    __shared__ __align__(16) StSmem sm;
+    pdl_trigger();
+    pdl_wait();
+    if (blockIdx.x < h_blocks) grad_tile<float, T, true, T>(dz, w, gh, blockIdx.x, sm);
+    else grad_tile<float, T, false, T>(dzt, h, gw, blockIdx.x - h_blocks, sm);
+}
+
 // out = sum of the splits' parts, in order, rounded once.
 template <class T>
 __global__ void __launch_bounds__(256) part_sum_kernel(const float *part, int splits, size_t n, T *out)
@@ -330,38 +349,6 @@ cudaError_t launch_part_sum(const float *part, int splits, size_t n, void *out, 
     return launch_k(part_sum_kernel<float>, grid, 256, 0, s, part, splits, n, (float *)out);
 }
 
-// The hidden rows with the rows that take no part zeroed, for dW = dz^T h: a
-// padding row's dz is zero, but zero times a NaN or an infinity in its
-// hidden row would not be.
-template <class T>
-__global__ void __launch_bounds__(256) clean_rows_kernel(const T *h, const int32_t *targets, const float *g, int N, int d,
-                                                         int V, T *out)
-{
-    pdl_trigger();
-    pdl_wait();
-    const int row = blockIdx.x;
-    const int t = targets[row];
-    const bool live = t >= 0 && t < V && g[row] != 0.f;
-    const T *src = h + (size_t)row * d;
-    T *dst = out + (size_t)row * d;
-    constexpr int E = 16 / (int)sizeof(T);
-    if (d % E == 0 && (((uintptr_t)src | (uintptr_t)dst) & 15) == 0) {
-        for (int i = threadIdx.x; i < d / E; i += 256)
-            ((uint4 *)dst)[i] = live ? ((const uint4 *)src)[i] : make_uint4(0, 0, 0, 0);
-    } else {
-        for (int i = threadIdx.x; i < d; i += 256) dst[i] = live ? src[i] : from_f<T>(0.f);
-    }
-}
-
-cudaError_t launch_clean_rows(const LossArgs &a, void *out, cudaStream_t s)
-{
-    if (a.dtype == ORTHRUS_BF16)
-        return launch_k(clean_rows_kernel<bf16>, a.N, 256, 0, s, (const bf16 *)a.h, a.targets, a.g, a.N, a.d, a.V,
-                        (bf16 *)out);
-    return launch_k(clean_rows_kernel<float>, a.N, 256, 0, s, (const float *)a.h, a.targets, a.g, a.N, a.d, a.V,
-                    (float *)out);
-}
-
 __global__ void __launch_bounds__(1024) zero_kernel(void *p, size_t bytes)
 {
     pdl_trigger();
@@ -374,10 +361,10 @@ __global__ void __launch_bounds__(1024) zero_kernel(void *p, size_t bytes)
 
 // ---------------------------------------------------------------- plans
 struct SimtPlan {
-    size_t total, o_dz, o_part, o_h;
+    size_t total, o_dz, o_part, o_alive;
     int piece, splits;
 };
-static SimtPlan plan_simt(int N, int d, int V, int es, int want_dw)
+static SimtPlan plan_simt(int N, int d, int V, int want_dw)
 {
     SimtPlan p{};
     WsPlan w;
@@ -390,7 +377,7 @@ static SimtPlan plan_simt(int N, int d, int V, int es, int want_dw)
     p.splits = (int)std::max<long>(1, std::min<long>({(2 * 148 + tiles - 1) / tiles, (p.piece + 255) / 256, 32L}));
     p.o_dz = w.take((size_t)N * p.piece * 4);
     p.o_part = w.take((size_t)p.splits * N * d * 4);
-    p.o_h = w.take(want_dw ? (size_t)N * d * es : 0);
+    p.o_alive = w.take(want_dw ? (size_t)N : 0);
     p.total = w.total;
     return p;
 }
@@ -406,7 +393,7 @@ size_t loss_fwd_workspace(int N, int d, int V, int dtype)
 
 size_t loss_grad_workspace(int N, int d, int V, int dtype, int want_dw, int kl)
 {
-    const size_t simt = plan_simt(N, d, V, dtype == ORTHRUS_BF16 ? 2 : 4, want_dw).total;
+    const size_t simt = plan_simt(N, d, V, want_dw).total;
     return dtype == ORTHRUS_BF16 && d % 8 == 0 ? std::max(simt, loss_grad_workspace_tc(N, d, V, want_dw, kl)) : simt;
 }
 
@@ -425,33 +412,32 @@ template <class T> static cudaError_t loss_fwd_simt(const LossArgs &a, cudaStrea
 
 template <class T> static cudaError_t loss_grad_simt(const LossArgs &a, cudaStream_t s)
 {
-    const SimtPlan p = plan_simt(a.N, a.d, a.V, (int)sizeof(T), a.dw != nullptr);
+    const SimtPlan p = plan_simt(a.N, a.d, a.V, a.dw != nullptr);
     float *dz = (float *)(a.ws + p.o_dz), *part = (float *)(a.ws + p.o_part);
-    T *hc = (T *)(a.ws + p.o_h);
+    unsigned char *alive = a.dw ? (unsigned char *)(a.ws + p.o_alive) : nullptr;
     const unsigned mt = (a.N + kSt - 1) / kSt, dt = (a.d + kSt - 1) / kSt;
-    cudaError_t e;
-    if (a.dw && (e = launch_clean_rows(a, hc, s)) != cudaSuccess) return e;
+    const bool direct = p.splits == 1 && p.piece >= a.V;   // dh in one share: no parts
     for (int v0 = 0; v0 < a.V; v0 += p.piece) {
         const int nv = std::min(p.piece, a.V - v0);
         const dim3 gz((nv + kSt - 1) / kSt, mt);
-        e = a.kl ? launch_k(dz_tile_simt<T, true>, gz, kStThreads, 0, s, a, v0, p.piece, dz)
-                 : launch_k(dz_tile_simt<T, false>, gz, kStThreads, 0, s, a, v0, p.piece, dz);
+        cudaError_t e = a.kl ? launch_k(dz_tile_simt<T, true>, gz, kStThreads, 0, s, a, v0, p.piece, dz, alive)
+                             : launch_k(dz_tile_simt<T, false>, gz, kStThreads, 0, s, a, v0, p.piece, dz, alive);
         if (e != cudaSuccess) return e;
-        const Operand<float> A{dz, (size_t)p.piece, 1, a.N};
-        const Operand<T> B{(const T *)a.w + (size_t)v0 * a.d, 1, (size_t)a.d, a.d};
+        const Operand<float> A{dz, (size_t)p.piece, 1, a.N, nullptr};
+        const Operand<T> B{(const T *)a.w + (size_t)v0 * a.d, 1, (size_t)a.d, a.d, nullptr};
         GradGemm g{};
-        g.M = a.N; g.N = a.d; g.K = nv; g.splits = p.splits; g.part = part; g.add = v0 > 0;
-        e = launch_k(grad_gemm_simt<float, T, true, T>, dim3(dt, mt, p.splits), kStThreads, 0, s, A, B, g);
-        if (e != cudaSuccess) return e;
-        if (!a.dw) continue;
-        const Operand<float> At{dz, 1, (size_t)p.piece, nv};
-        const Operand<T> Bh{hc, 1, (size_t)a.d, a.d};
+        g.M = a.N; g.N = a.d; g.K = nv; g.splits = p.splits; g.part = direct ? nullptr : part; g.add = v0 > 0; g.out = a.dh;
+        // a padding row's dz is zero, but zero times a NaN or an infinity in its
+        // hidden row would not be: dW skips the rows that take no part
+        const Operand<float> At{dz, 1, (size_t)p.piece, nv, nullptr};
+        const Operand<T> Bh{(const T *)a.h, 1, (size_t)a.d, a.d, alive};
         GradGemm gw{};
-        gw.M = nv; gw.N = a.d; gw.K = a.N; gw.splits = 1; gw.out = (T *)a.dw + (size_t)v0 * a.d;
-        e = launch_k(grad_gemm_simt<float, T, false, T>, dim3(dt, (nv + kSt - 1) / kSt, 1), kStThreads, 0, s, At, Bh, gw);
+        gw.M = nv; gw.N = a.d; gw.K = a.N; gw.splits = 1; gw.out = a.dw ? (T *)a.dw + (size_t)v0 * a.d : nullptr;
+        const unsigned hb = dt * mt * p.splits, wb = a.dw ? dt * ((nv + kSt - 1) / kSt) : 0;
+        e = launch_k(grads_simt<T>, hb + wb, kStThreads, 0, s, A, B, g, hb, At, Bh, gw);
         if (e != cudaSuccess) return e;
     }
-    return launch_part_sum(part, p.splits, (size_t)a.N * a.d, a.dh, a.dtype, s);
+    return direct ? cudaSuccess : launch_part_sum(part, p.splits, (size_t)a.N * a.d, a.dh, a.dtype, s);
 }
 
 cudaError_t launch_loss_fwd(const LossArgs &a, cudaStream_t s)

@@ -50,14 +50,13 @@ constexpr uint32_t kVlABytes = 128 * kVlK * 2; // A bytes of a CTA's stage
 constexpr int kVlStages = 6;                   // most ring stages (3 at bn = 256)
 constexpr uint32_t kVlRing = 221184;           // bytes of the ring: 3 stages of 64 KiB, or 6 at bn = 32
 constexpr int kVlPairs = 74;                   // 2-CTA clusters that fit at once on 148 SMs
-constexpr int kVlJobs = 3;
 constexpr long long kVlSpinCycles = 4000000000LL;   // ~2 s at the B200 SM clock
 constexpr float kLog2e = 1.4426950408889634f;
 
 enum VlKind : int { VL_LSE = 0, VL_DZ = 1, VL_DZKL = 2, VL_DH = 3, VL_DW = 4, VL_LSE_T = 5, VL_DZ_T = 6, VL_DZKL_T = 7,
                     VL_DH_T = 8 };
 
-// One product of a launch: mt x nt x splits tiles.
+// The product of a launch: mt x nt x splits tiles; pair p takes tiles p, p + pairs, ..
 struct VlJob {
     CUtensorMap a, b;
     int kind;
@@ -79,12 +78,10 @@ struct VlJob {
     bf16 *out;           // DH: [M][N]; DW: [M][N]
 };
 struct VlParams {
-    VlJob job[kVlJobs];
-    int jobs, pairs, stages;
+    VlJob job;
+    int pairs, stages;
     uint32_t stage_bytes;
     unsigned *err;
-    // job 0: tiles p, p + pairs, ..; job j > 0: tiles [first[j][p], first[j][p + 1])
-    uint16_t first[kVlJobs][kVlPairs + 1];
 };
 
 // ---------------------------------------------------------------- PTX wrappers
@@ -204,44 +201,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 
 // ---------------------------------------------------------------- tiles
 struct VlTile {
-    int m0, n0, nt, split, c0, c1;   // first row and column, column tile, k chunks [c0, c1)
+    int m0, n0, nt, split, c0, dc, nc;   // first row and column, column tile, k chunks c0, c0 + dc, .. (nc of them)
 };
-// The tiles of pair p, in order, over all jobs of the launch.
-struct VlIter {
-    const VlParams &prm;
-    int p, j, t, end, step;
-    __device__ VlIter(const VlParams &prm_, int p_) : prm(prm_), p(p_), j(-1), t(0), end(0), step(1) { next_job(); }
-    __device__ void next_job()
-    {
-        while (++j < prm.jobs) {
-            const VlJob &jb = prm.job[j];
-            if (j == 0) { t = p; step = prm.pairs; end = jb.mt * jb.nt * jb.splits; }
-            else { t = prm.first[j][p]; step = 1; end = prm.first[j][p + 1]; }
-            if (t < end) return;
-        }
-    }
-    __device__ bool valid() const { return j < prm.jobs; }
-    __device__ VlTile get() const
-    {
-        const VlJob &jb = prm.job[j];
-        VlTile x;
-        int r = t, m, n;
-        if (jb.n_fast) { n = r % jb.nt; r /= jb.nt; m = r % jb.mt; r /= jb.mt; }
-        else { m = r % jb.mt; r /= jb.mt; n = r % jb.nt; r /= jb.nt; }
-        x.m0 = m * kVlM;
-        x.n0 = n * jb.bn;
-        x.nt = n;
-        x.split = r;
-        x.c0 = (int)((long)jb.chunks * r / jb.splits);
-        x.c1 = (int)((long)jb.chunks * (r + 1) / jb.splits);
-        return x;
-    }
-    __device__ void advance()
-    {
-        t += step;
-        if (t >= end) next_job();
-    }
-};
+__device__ __forceinline__ VlTile vl_tile(const VlJob &jb, int t)
+{
+    VlTile x;
+    int m, n;
+    if (jb.n_fast) { n = t % jb.nt; t /= jb.nt; m = t % jb.mt; t /= jb.mt; }
+    else { m = t % jb.mt; t /= jb.mt; n = t % jb.nt; t /= jb.nt; }
+    x.m0 = m * kVlM;
+    x.n0 = n * jb.bn;
+    x.nt = n;
+    x.split = t;
+    // dh walks the ids backwards, all shares together: the rows of W that dz
+    // read last are still in L2
+    const bool back = jb.kind == VL_DH || jb.kind == VL_DH_T;
+    x.c0 = back ? jb.chunks - 1 - t : 0;
+    x.dc = back ? -jb.splits : 1;
+    x.nc = back ? (jb.chunks - t + jb.splits - 1) / jb.splits : jb.chunks;
+    return x;
+}
 
 struct VlSmem {
     alignas(8) uint64_t full[kVlStages], empty[kVlStages], tfull[2], tempty[2];
@@ -539,27 +518,27 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
     vl_fence_after();
     const uint32_t tmem = sm.tmem_base;
     pdl_wait();
-    for (int j = 0; j < prm.jobs; ++j)   // (at most one job of a launch has columns)
-        if (prm.job[j].kind == VL_DZ_T || prm.job[j].kind == VL_DZKL_T) {
-            vl_columns(prm.job[j], sm, prm.err);
-            __syncthreads();
-        }
+    const VlJob &jb = prm.job;
+    const int tiles = jb.mt * jb.nt * jb.splits;
+    if (jb.kind == VL_DZ_T || jb.kind == VL_DZKL_T) {
+        vl_columns(jb, sm, prm.err);
+        __syncthreads();
+    }
 
     if (warp == 0) {
         if (lane == 0) {   // ------------------------------------------- producer
             uint32_t stage = 0, phase = 0;
             bool stop = false;
-            for (VlIter it(prm, pair); it.valid() && !stop; it.advance()) {
-                const VlJob &jb = prm.job[it.j];
-                const VlTile x = it.get();
+            for (int t = pair; t < tiles && !stop; t += prm.pairs) {
+                const VlTile x = vl_tile(jb, t);
                 const int am = x.m0 + (int)rank * 128, bnh = jb.bn / 2, bx = x.n0 + (int)rank * bnh;
                 const uint32_t bytes = 2 * (kVlABytes + (uint32_t)bnh * kVlK * 2);
-                for (int c = x.c0; c < x.c1; ++c) {
+                for (int i = 0; i < x.nc; ++i) {
                     if (!vl_wait(&sm.empty[stage], phase ^ 1, abort) || *abort) { stop = true; break; }
                     if (rank == 0) vl_expect_tx(&sm.full[stage], bytes);
                     const uint32_t bar = vl_mapa(smem_u32(&sm.full[stage]), 0);
                     const uint32_t a = ring + stage * prm.stage_bytes, b = a + kVlABytes;
-                    const int k = c * kVlK;
+                    const int k = (x.c0 + i * x.dc) * kVlK;
                     // two boxes of 64 elements each: along k (K-major), or along M / N
                     if (jb.a_mn) {
                         vl_load(a, &jb.a, am, jb.a_off + k, bar);
@@ -584,9 +563,8 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
         if (lane == 0 && rank == 0) {   // ------------------------------ MMA issuer
             uint32_t stage = 0, phase = 0;
             int local = 0;
-            for (VlIter it(prm, pair); it.valid() && !*abort; it.advance(), ++local) {
-                const VlJob &jb = prm.job[it.j];
-                const VlTile x = it.get();
+            for (int t = pair; t < tiles && !*abort; t += prm.pairs, ++local) {
+                const VlTile x = vl_tile(jb, t);
                 const int acc = local & 1;
                 const bool a_mn = jb.a_mn, b_mn = jb.b_mn;
                 const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
@@ -599,7 +577,7 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
                 vl_fence_after();
                 const uint32_t d = tmem + acc * kVlNMax;
                 bool ok = true;
-                for (int c = x.c0; c < x.c1; ++c) {
+                for (int i = 0; i < x.nc; ++i) {
                     if (!vl_wait(&sm.full[stage], phase, abort)) { ok = false; break; }
                     vl_fence_after();
                     const uint32_t a = ring + stage * prm.stage_bytes, b = a + kVlABytes;
@@ -607,7 +585,7 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
 #pragma unroll
                     for (int k = 0; k < kVlK / 16; ++k)
                         vl_mma(d, ad + as * (k & 3) + ah * (k >> 2), bd + bs * (k & 3) + bh * (k >> 2), idesc,
-                               (c > x.c0 || k > 0) ? 1u : 0u);
+                               (i > 0 || k > 0) ? 1u : 0u);
                     vl_commit(&sm.empty[stage]);
                     if (++stage == (uint32_t)prm.stages) { stage = 0; phase ^= 1; }
                 }
@@ -621,9 +599,8 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
         const int r = (int)rank * 128 + q * 32 + lane;   // row in the tile
         const uint32_t free0 = vl_mapa(smem_u32(&sm.tempty[0]), 0), free1 = vl_mapa(smem_u32(&sm.tempty[1]), 0);
         int local = 0;
-        for (VlIter it(prm, pair); it.valid(); it.advance(), ++local) {
-            const VlJob &jb = prm.job[it.j];
-            const VlTile x = it.get();
+        for (int t = pair; t < tiles; t += prm.pairs, ++local) {
+            const VlTile x = vl_tile(jb, t);
             const int acc = local & 1, row = x.m0 + r;
             const bool ok = vl_wait(&sm.tfull[acc], (local >> 1) & 1, abort);
             if (!__all_sync(0xffffffffu, ok)) break;
@@ -680,6 +657,20 @@ __global__ void __launch_bounds__(256) vl_interleave_kernel(const uint4 *ra, con
     }
 }
 
+// The hidden rows with the rows that take no part zeroed, for dW = dz^T h: a
+// padding row's dz is zero, but zero times a NaN or an infinity in its
+// hidden row would not be.
+__global__ void __launch_bounds__(256) vl_clean_kernel(const uint4 *h, const int32_t *targets, const float *g, int V,
+                                                       uint4 *out, int vecs)
+{
+    pdl_trigger();
+    pdl_wait();
+    const int r = blockIdx.x, t = targets[r];
+    const bool live = t >= 0 && t < V && g[r] != 0.f;
+    for (int i = threadIdx.x; i < vecs; i += 256)
+        out[(size_t)r * vecs + i] = live ? h[(size_t)r * vecs + i] : make_uint4(0, 0, 0, 0);
+}
+
 // ---------------------------------------------------------------- host
 static size_t up(size_t x, size_t m) { return (x + m - 1) / m * m; }
 
@@ -710,14 +701,9 @@ bool loss_tc_ok(const LossArgs &a)
 
 static cudaError_t vl_launch(VlParams &p, cudaStream_t s)
 {
-    long tiles = 0;
-    int bn = 0;
-    for (int j = 0; j < p.jobs; ++j) {
-        tiles += (long)p.job[j].mt * p.job[j].nt * p.job[j].splits;
-        bn = std::max(bn, p.job[j].bn);
-    }
-    p.pairs = (int)std::min<long>(kVlPairs, tiles);
-    p.stage_bytes = kVlABytes + (uint32_t)bn / 2 * kVlK * 2;
+    const VlJob &j = p.job;
+    p.pairs = (int)std::min<long>(kVlPairs, (long)j.mt * j.nt * j.splits);
+    p.stage_bytes = kVlABytes + (uint32_t)j.bn / 2 * kVlK * 2;
     p.stages = (int)std::min<uint32_t>(kVlStages, kVlRing / p.stage_bytes);
     const size_t smem = 1024 + kVlRing;
     cudaError_t e = cudaFuncSetAttribute(vocab_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -753,7 +739,7 @@ cudaError_t loss_fwd_tc(const LossArgs &a, cudaStream_t s)
     float *zt = (float *)(a.ws + loss_fwd_workspace_tc(a.N, a.d, a.V) - (((size_t)a.N * 4 + 255) & ~(size_t)255));
     VlParams p;
     memset(&p, 0, sizeof(p));
-    VlJob &j = p.job[0];
+    VlJob &j = p.job;
     const bool narrow = vl_narrow(a.N);
     const int rows = narrow ? a.V : a.N, cols = narrow ? a.N : a.V;
     j.kind = narrow ? VL_LSE_T : VL_LSE; j.M = rows; j.N = cols; j.chunks = (a.d + kVlK - 1) / kVlK; j.splits = 1;
@@ -763,7 +749,7 @@ cudaError_t loss_fwd_tc(const LossArgs &a, cudaStream_t s)
     if (!make_tmap_box(&j.a, narrow ? a.w : a.h, rows, a.d, 64, 128) ||
         !make_tmap_box(&j.b, narrow ? a.h : a.w, cols, a.d, 64, j.bn / 2))
         return cudaErrorInvalidValue;
-    p.jobs = 1; p.err = a.err;
+    p.err = a.err;
     cudaError_t e = vl_launch(p, s);
     if (e != cudaSuccess) return e;
     return launch_ce_finalize(rec, zt, a, narrow ? (a.V + 31) / 32 : j.nt, 1, s);
@@ -806,7 +792,7 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
     if (a.kl)
         e = launch_k(vl_interleave_kernel, N, 256, 0, s, (const uint4 *)a.h, (const uint4 *)a.h2, a.g, (uint4 *)hx, d / 8);
     else if (a.dw)
-        e = launch_clean_rows(a, hx, s);
+        e = launch_k(vl_clean_kernel, N, 256, 0, s, (const uint4 *)a.h, a.targets, a.g, a.V, (uint4 *)hx, d / 8);
     if (e != cudaSuccess) return e;
     const int zbn = pl.z_narrow ? vl_narrow_bn(pl.zrows) : kVlNMax, hbn = pl.h_narrow ? vl_narrow_bn(N) : kVlNMax;
     // zh: hidden rows, zw: head rows (both along k); dzk: dz along its ids; wm:
@@ -823,7 +809,7 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
         const int nv = std::min(pl.piece, a.V - v0);
         {
             memset(&p, 0, sizeof(p));
-            VlJob &j = p.job[0];
+            VlJob &j = p.job;
             j.kind = a.kl ? (pl.z_narrow ? VL_DZKL_T : VL_DZKL) : (pl.z_narrow ? VL_DZ_T : VL_DZ);
             j.M = pl.z_narrow ? nv : pl.zrows; j.N = pl.z_narrow ? pl.zrows : nv;
             j.chunks = (d + kVlK - 1) / kVlK; j.splits = 1; j.bn = zbn;
@@ -832,12 +818,12 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
             j.targets = a.targets; j.lse = a.lse_in; j.lse2 = a.lse2_in; j.g = a.g;
             j.dz = dz; j.v0 = v0; j.V = a.V; j.pitch = pl.piece;
             j.a = pl.z_narrow ? zw : zh; j.b = pl.z_narrow ? zh : zw;
-            p.jobs = 1; p.err = a.err;
+            p.err = a.err;
             if ((e = vl_launch(p, s)) != cudaSuccess) return e;
         }
         {
             memset(&p, 0, sizeof(p));
-            VlJob &j = p.job[0];
+            VlJob &j = p.job;
             j.kind = pl.h_narrow ? VL_DH_T : VL_DH;
             j.M = pl.h_narrow ? d : N; j.N = pl.h_narrow ? N : d; j.chunks = (nv + kVlK - 1) / kVlK;
             j.splits = std::min(pl.splits, j.chunks);
@@ -846,18 +832,18 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
             (pl.h_narrow ? j.a_off : j.b_off) = v0;
             j.part = part; j.add = v0 > 0; j.last = pl.splits == 1 && v0 + pl.piece >= a.V; j.out = (bf16 *)a.dh;
             j.a = pl.h_narrow ? wm : dzk; j.b = pl.h_narrow ? dzk : wm;
-            p.jobs = 1; p.err = a.err;
+            p.err = a.err;
             if ((e = vl_launch(p, s)) != cudaSuccess) return e;
         }
         if (a.dw) {
             memset(&p, 0, sizeof(p));
-            VlJob &j = p.job[0];
+            VlJob &j = p.job;
             j.kind = VL_DW; j.M = nv; j.N = d; j.chunks = (N + kVlK - 1) / kVlK; j.splits = 1;
             j.bn = 256; j.mt = (nv + kVlM - 1) / kVlM; j.nt = (d + 255) / 256; j.n_fast = 1;
             j.a_mn = j.b_mn = 1;
             j.out = (bf16 *)a.dw + (size_t)v0 * d;
             j.a = dzm; j.b = hm;
-            p.jobs = 1; p.err = a.err;
+            p.err = a.err;
             if ((e = vl_launch(p, s)) != cudaSuccess) return e;
         }
     }
