@@ -23,7 +23,8 @@
 //               shared-memory stages; both CTAs' loads count on the first
 //               CTA's mbarrier
 //   warp 1      MMA issuer (first CTA of the pair only)
-//   warps 4..7  epilogue: one accumulator row per thread, 32 columns at a time
+//   warps 4..11 epilogue: one accumulator row per thread, 32 columns at a time;
+//               two warps share 32 rows and take every other 32 columns
 //
 // Two accumulators (2 x 256 TMEM columns) let the next tile's MMAs run under
 // an epilogue.  Every wait is bounded: on timeout the kernel raises
@@ -41,14 +42,15 @@ namespace orthrus {
 
 bool make_tmap_box(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows);
 
-constexpr int kVlThreads = 256;
-constexpr int kVlEpi = 128;                    // epilogue threads per CTA
+constexpr int kVlThreads = 384;
+constexpr int kVlEpi = 256;                    // epilogue threads per CTA
 constexpr int kVlM = 256;                      // rows of a pair's tile
 constexpr int kVlNMax = 256;                   // columns of a pair's tile
 constexpr int kVlK = 128;                      // k per stage: eight MMAs for each wait and commit
 constexpr uint32_t kVlABytes = 128 * kVlK * 2; // A bytes of a CTA's stage
 constexpr int kVlStages = 6;                   // most ring stages (3 at bn = 256)
-constexpr uint32_t kVlRing = 221184;           // bytes of the ring: 3 stages of 64 KiB, or 6 at bn = 32
+constexpr uint32_t kVlRing = 221184;           // most bytes of the ring: 3 stages of 64 KiB, or 6 at bn = 32
+constexpr uint32_t kVlShared = 229376;         // the ring and what an epilogue keeps behind it
 constexpr int kVlPairs = 74;                   // 2-CTA clusters that fit at once on 148 SMs
 constexpr long long kVlSpinCycles = 4000000000LL;   // ~2 s at the B200 SM clock
 constexpr float kLog2e = 1.4426950408889634f;
@@ -58,7 +60,7 @@ enum VlKind : int { VL_LSE = 0, VL_DZ = 1, VL_DZKL = 2, VL_DH = 3, VL_DW = 4, VL
 
 // The product of a launch: mt x nt x splits tiles; pair p takes tiles p, p + pairs, ..
 struct VlJob {
-    CUtensorMap a, b;
+    CUtensorMap a, b, c;   // c (DW): the result, boxes of 64 columns x 32 rows
     int kind;
     int M, N;            // valid rows and columns of the result
     int chunks, splits;  // k chunks of kVlK, and the shares they are cut into (DH)
@@ -75,7 +77,8 @@ struct VlJob {
     int v0, V, pitch;    // DZ: the piece's first id, the vocabulary, dz's row length
     float *part;         // DH: [splits][M][N] fp32
     int add, last;       // DH: add to part; the last piece of an unsplit dh: write out
-    bf16 *out;           // DH: [M][N]; DW: [M][N]
+    bf16 *out;           // DH: [M][N]
+    int c_off;           // DW: first row of the result
 };
 struct VlParams {
     VlJob job;
@@ -224,21 +227,34 @@ __device__ __forceinline__ VlTile vl_tile(const VlJob &jb, int t)
 
 struct VlSmem {
     alignas(8) uint64_t full[kVlStages], empty[kVlStages], tfull[2], tempty[2];
+    uint64_t half[2][4];   // LSE: the second warp of a quarter left its part (per accumulator)
     uint32_t tmem_base;
     int abort;
-    // transposed kinds: per column (row of h) lse * log2 e, upstream gradient, target
-    float col_k[kVlNMax], col_g[kVlNMax];
-    int col_t[kVlNMax];
 };
+// Behind the ring: LSE, the second warps' (maximum, sum) of a tile, per
+// accumulator; the transposed kinds, per column (row of h) lse * log2 e,
+// upstream gradient and target; DW, 4 KiB per epilogue warp.
+union VlTail {
+    float2 half[2][128];
+    struct {
+        float k[kVlNMax], g[kVlNMax];
+        int t[kVlNMax];
+    } col;
+    unsigned char store[kVlEpi / 32][4096];
+};
+static_assert(kVlRing + sizeof(((VlTail *)0)->col) <= kVlShared && 3 * 65536 + sizeof(VlTail) <= kVlShared, "shared memory");
 
 // ---------------------------------------------------------------- epilogues
-// taddr: the accumulator's first column, this warp's lanes.
-__device__ __forceinline__ void vl_epi_lse(const VlJob &jb, const VlTile &x, int row, uint32_t taddr)
+// taddr: the accumulator's first column, this warp's lanes; half: which of the
+// two warps of these rows.
+// false: the other warp's part did not come (the kernel is giving up)
+__device__ __forceinline__ bool vl_epi_lse(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, int half, float2 *other,
+                                           uint64_t *bar, uint32_t parity, volatile int *abort)
 {
     const int nv = min(jb.bn, jb.N - x.n0);           // ids of this tile below the vocabulary
     const int id = row < jb.M ? jb.targets[row] : -1, t = id < 0 ? -1 : id - x.n0;
     float m = -INFINITY, s = 0.f, z_t = 0.f;
-    for (int c = 0; c < nv; c += 32) {
+    for (int c = 32 * half; c < nv; c += 64) {
         float r[32];
         vl_tmem_ld32(taddr + c, r);
         if (nv - c < 32)
@@ -259,10 +275,24 @@ __device__ __forceinline__ void vl_epi_lse(const VlJob &jb, const VlTile &x, int
         s = (a[0] + a[1]) + (a[2] + a[3]);
         m = mn;
     }
-    if (row < jb.M) {
-        jb.rec[(size_t)x.nt * jb.M + row] = make_float2(m, s);
-        if (t >= 0 && t < nv) jb.zt[row] = z_t;
+    // (the buffer of this accumulator is free: the MMAs of the tile needed both
+    // warps' arrival after its last use)
+    if (half) {
+        *other = make_float2(m, s);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+    } else if (!__all_sync(0xffffffffu, vl_wait(bar, parity, abort))) {
+        return false;
     }
+    if (row < jb.M && t >= 0 && t < nv && (t >> 5 & 1) == half) jb.zt[row] = z_t;
+    if (row < jb.M && !half) {
+        const float2 o = *other;
+        const float mn = fmaxf(m, o.x), k = (mn == -INFINITY ? 0.f : mn) * kLog2e;
+        s = s * vl_exp2(fmaf(m, kLog2e, -k)) + o.y * vl_exp2(fmaf(o.x, kLog2e, -k));
+        jb.rec[(size_t)x.nt * jb.M + row] = make_float2(mn, s);
+    }
+    return true;
 }
 
 // 16 bf16 columns of a row of dz
@@ -272,20 +302,20 @@ __device__ __forceinline__ void vl_store16(bf16 *p, const float (&v)[16])
     ((uint4 *)p)[1] = make_uint4(pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]), pack_bf16(v[12], v[13]), pack_bf16(v[14], v[15]));
 }
 
-__device__ __forceinline__ void vl_epi_dz(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, unsigned *err)
+__device__ __forceinline__ void vl_epi_dz(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, int half, unsigned *err)
 {
     float g = 0.f, k = 0.f;
     int t = -1;
     if (row < jb.M) {
         const int id = jb.targets[row];
-        if (id >= jb.V && x.n0 == 0 && jb.v0 == 0 && err) raise_err(err, ORTHRUS_DEVERR_TOKEN);
+        if (id >= jb.V && x.n0 == 0 && jb.v0 == 0 && half == 0 && err) raise_err(err, ORTHRUS_DEVERR_TOKEN);
         if (id >= 0 && id < jb.V) { g = jb.g[row]; t = id - jb.v0 - x.n0; }
         k = jb.lse[row] * kLog2e;
     }
     const int nv = jb.N - x.n0;                        // columns of the tile below the piece's end (may exceed bn)
     const int nc = min(jb.bn, jb.pitch - x.n0);        // columns dz has room for
     bf16 *dst = jb.dz + (size_t)row * jb.pitch + x.n0;
-    for (int c = 0; c < nc; c += 32) {
+    for (int c = 32 * half; c < nc; c += 64) {
         float r[32];
         vl_tmem_ld32(taddr + c, r);
         if (row >= jb.M) continue;
@@ -307,7 +337,7 @@ __device__ __forceinline__ void vl_epi_dz(const VlJob &jb, const VlTile &x, int 
 // Interleaved rows: even lanes hold the AR view's logits of a position, odd
 // lanes the diffusion view's.  Each pair of lanes exchanges halves of a chunk
 // and writes 16 columns per lane.
-__device__ __forceinline__ void vl_epi_dzkl(const VlJob &jb, const VlTile &x, int row, uint32_t taddr)
+__device__ __forceinline__ void vl_epi_dzkl(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, int half)
 {
     const int pos = row >> 1, odd = row & 1;
     const bool live = row < jb.M;
@@ -315,7 +345,7 @@ __device__ __forceinline__ void vl_epi_dzkl(const VlJob &jb, const VlTile &x, in
     const int nv = jb.N - x.n0;
     const int nc = min(jb.bn, jb.pitch - x.n0);
     bf16 *dst = jb.dz + (size_t)pos * jb.pitch + x.n0 + 16 * odd;
-    for (int c = 0; c < nc; c += 32) {
+    for (int c = 32 * half; c < nc; c += 64) {
         float r[32], v[16];
         vl_tmem_ld32(taddr + c, r);
 #pragma unroll
@@ -332,13 +362,13 @@ __device__ __forceinline__ void vl_epi_dzkl(const VlJob &jb, const VlTile &x, in
 }
 
 // dh: this piece's share, added to what earlier pieces left
-__device__ __forceinline__ void vl_epi_dh(const VlJob &jb, const VlTile &x, int row, uint32_t taddr)
+__device__ __forceinline__ void vl_epi_dh(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, int half)
 {
     const int nv = min(jb.bn, jb.N - x.n0);            // (a multiple of 8)
     const bool out = jb.last;
     float *p = jb.part + ((size_t)x.split * jb.M + row) * jb.N + x.n0;
     bf16 *o = jb.out + (size_t)row * jb.N + x.n0;
-    for (int c = 0; c < nv; c += 32) {
+    for (int c = 32 * half; c < nv; c += 64) {
         float r[32];
         vl_tmem_ld32(taddr + c, r);
         if (row >= jb.M) continue;
@@ -359,28 +389,44 @@ __device__ __forceinline__ void vl_epi_dh(const VlJob &jb, const VlTile &x, int 
     }
 }
 
-__device__ __forceinline__ void vl_epi_dw(const VlJob &jb, const VlTile &x, int row, uint32_t taddr)
+// dW leaves by TMA: 64 columns x 32 rows at a time through shared memory, whole
+// 128-byte lines (16-byte stores of a row per thread took DW_BEFORE us for the dW of
+// 31 rows of 2048, vocabulary 151936; this takes DW_AFTER us).  The map clips what lies
+// past the last row or column.
+__device__ __forceinline__ void vl_epi_dw(const VlJob &jb, const VlTile &x, int row0, int lane, uint32_t taddr,
+                                          int half, uint32_t buf)
 {
     const int nv = min(jb.bn, jb.N - x.n0);
-    bf16 *o = jb.out + (size_t)row * jb.N + x.n0;
-    for (int c = 0; c < nv; c += 32) {
-        float r[32];
-        vl_tmem_ld32(taddr + c, r);
-        if (row >= jb.M) continue;
+    const uint32_t dst = buf + lane * 128;
+    for (int c = 64 * half; c < nv; c += 128) {
+        asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
 #pragma unroll
-        for (int q = 0; q < 32; q += 8) {
-            if (c + q >= nv) break;
-            *(uint4 *)(o + c + q) = make_uint4(pack_bf16(r[q], r[q + 1]), pack_bf16(r[q + 2], r[q + 3]),
-                                               pack_bf16(r[q + 4], r[q + 5]), pack_bf16(r[q + 6], r[q + 7]));
+        for (int h = 0; h < 2; ++h) {
+            float r[32];
+            vl_tmem_ld32(taddr + c + 32 * h, r);   // (its warp sync orders lane 0's wait before the stores)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + (((4 * h + i) ^ (lane & 7)) << 4)),
+                             "r"(pack_bf16(r[8 * i], r[8 * i + 1])), "r"(pack_bf16(r[8 * i + 2], r[8 * i + 3])),
+                             "r"(pack_bf16(r[8 * i + 4], r[8 * i + 5])), "r"(pack_bf16(r[8 * i + 6], r[8 * i + 7]))
+                             : "memory");
+        }
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n"
+                         "cp.async.bulk.commit_group;\n" ::"l"((uint64_t)&jb.c), "r"(x.n0 + c), "r"(jb.c_off + row0), "r"(dst)
+                         : "memory");
         }
     }
 }
 
 // ---- transposed: a thread holds one id (or one hidden column), 32 rows at a time
 // the columns' constants, one column per thread
-__device__ __forceinline__ void vl_columns(const VlJob &jb, VlSmem &sm, unsigned *err)
+__device__ __forceinline__ void vl_columns(const VlJob &jb, VlTail &tail, unsigned *err)
 {
     const int c = threadIdx.x;
+    if (c >= kVlNMax) return;
     float k = 0.f, g = 0.f;
     int t = -1;
     if (c < jb.N) {
@@ -394,11 +440,11 @@ __device__ __forceinline__ void vl_columns(const VlJob &jb, VlSmem &sm, unsigned
             if (t >= jb.V && blockIdx.x == 0 && err) raise_err(err, ORTHRUS_DEVERR_TOKEN);
         }
     }
-    sm.col_k[c] = k;
-    sm.col_g[c] = g;
-    sm.col_t[c] = t;
+    tail.col.k[c] = k;
+    tail.col.g[c] = g;
+    tail.col.t[c] = t;
 }
-static_assert(kVlThreads == kVlNMax, "one column per thread");
+static_assert(kVlThreads >= kVlNMax, "one column per thread");
 
 __device__ __forceinline__ float warp_max_f32(float v)
 {
@@ -409,9 +455,9 @@ __device__ __forceinline__ float warp_max_f32(float v)
 
 // v: this thread's id (the tile's ids are in order, so a warp holds one group
 // of 32); a record per (group, row).
-__device__ __forceinline__ void vl_epi_lse_t(const VlJob &jb, int v, uint32_t taddr, int lane)
+__device__ __forceinline__ void vl_epi_lse_t(const VlJob &jb, int v, uint32_t taddr, int half, int lane)
 {
-    for (int c = 0; c < jb.N; c += 32) {
+    for (int c = 32 * half; c < jb.N; c += 64) {
         float r[32], m = -INFINITY;
         vl_tmem_ld32(taddr + c, r);
         const int tgt = c + lane < jb.N ? jb.targets[c + lane] : -1;
@@ -438,44 +484,44 @@ __device__ __forceinline__ void vl_epi_lse_t(const VlJob &jb, int v, uint32_t ta
 
 // i: this thread's id within the piece; jb.M ids of the piece are real, the
 // rest of dz's row length gets zeros
-__device__ __forceinline__ void vl_epi_dz_t(const VlJob &jb, const VlSmem &sm, int i, uint32_t taddr)
+__device__ __forceinline__ void vl_epi_dz_t(const VlJob &jb, const VlTail &tail, int i, uint32_t taddr, int half)
 {
     const int v = jb.v0 + i;
     const bool live = i < jb.M;
-    for (int c = 0; c < jb.N; c += 32) {
+    for (int c = 32 * half; c < jb.N; c += 64) {
         float r[32];
         vl_tmem_ld32(taddr + c, r);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
             if (c + j >= jb.N) break;
-            const float g = sm.col_g[c + j];
-            float e = vl_exp2(fmaf(r[j], kLog2e, -sm.col_k[c + j]));
-            if (sm.col_t[c + j] == v) e -= 1.f;
+            const float g = tail.col.g[c + j];
+            float e = vl_exp2(fmaf(r[j], kLog2e, -tail.col.k[c + j]));
+            if (tail.col.t[c + j] == v) e -= 1.f;
             jb.dz[(size_t)(c + j) * jb.pitch + i] = __float2bfloat16_rn(g == 0.f || !live ? 0.f : g * e);
         }
     }
 }
 
-__device__ __forceinline__ void vl_epi_dzkl_t(const VlJob &jb, const VlSmem &sm, int i, uint32_t taddr)
+__device__ __forceinline__ void vl_epi_dzkl_t(const VlJob &jb, const VlTail &tail, int i, uint32_t taddr, int half)
 {
     const bool live = i < jb.M;
-    for (int c = 0; c < jb.N; c += 32) {
+    for (int c = 32 * half; c < jb.N; c += 64) {
         float r[32];
         vl_tmem_ld32(taddr + c, r);
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
             if (c + j >= jb.N) break;
-            const float g = sm.col_g[c + j];
-            const float pa = vl_exp2(fmaf(r[j], kLog2e, -sm.col_k[c + j]));
-            const float pd = vl_exp2(fmaf(r[j + 1], kLog2e, -sm.col_k[c + j + 1]));
+            const float g = tail.col.g[c + j];
+            const float pa = vl_exp2(fmaf(r[j], kLog2e, -tail.col.k[c + j]));
+            const float pd = vl_exp2(fmaf(r[j + 1], kLog2e, -tail.col.k[c + j + 1]));
             jb.dz[(size_t)((c + j) >> 1) * jb.pitch + i] = __float2bfloat16_rn(g == 0.f || !live ? 0.f : g * (pd - pa));
         }
     }
 }
 
-__device__ __forceinline__ void vl_epi_dh_t(const VlJob &jb, const VlTile &x, int i, uint32_t taddr)
+__device__ __forceinline__ void vl_epi_dh_t(const VlJob &jb, const VlTile &x, int i, uint32_t taddr, int half)
 {
-    for (int c = 0; c < jb.N; c += 32) {
+    for (int c = 32 * half; c < jb.N; c += 64) {
         float r[32];
         vl_tmem_ld32(taddr + c, r);
         if (i >= jb.M) continue;
@@ -500,10 +546,12 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
     const uint32_t rank = blockIdx.x & 1;               // CTA of the pair
     const int pair = blockIdx.x >> 1;
     volatile int *abort = &sm.abort;
+    VlTail &tail = *(VlTail *)(vl_smem_raw + (ring - smem_u32(vl_smem_raw)) + prm.stages * prm.stage_bytes);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kVlStages; ++s) { vl_mbar_init(&sm.full[s], 1); vl_mbar_init(&sm.empty[s], 1); }
         for (int s = 0; s < 2; ++s) { vl_mbar_init(&sm.tfull[s], 1); vl_mbar_init(&sm.tempty[s], 2 * kVlEpi / 32); }
+        for (int s = 0; s < 8; ++s) vl_mbar_init(&sm.half[s >> 2][s & 3], 1);
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -521,7 +569,7 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
     const VlJob &jb = prm.job;
     const int tiles = jb.mt * jb.nt * jb.splits;
     if (jb.kind == VL_DZ_T || jb.kind == VL_DZKL_T) {
-        vl_columns(jb, sm, prm.err);
+        vl_columns(jb, tail, prm.err);
         __syncthreads();
     }
 
@@ -598,11 +646,13 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
         const int q = warp & 3;                          // TMEM lane quarter of this warp
         const int r = (int)rank * 128 + q * 32 + lane;   // row in the tile
         const uint32_t free0 = vl_mapa(smem_u32(&sm.tempty[0]), 0), free1 = vl_mapa(smem_u32(&sm.tempty[1]), 0);
+        const int half = (warp - 4) >> 2;
         int local = 0;
         for (int t = pair; t < tiles; t += prm.pairs, ++local) {
             const VlTile x = vl_tile(jb, t);
             const int acc = local & 1, row = x.m0 + r;
-            const bool ok = vl_wait(&sm.tfull[acc], (local >> 1) & 1, abort);
+            const uint32_t parity = (local >> 1) & 1;
+            bool ok = vl_wait(&sm.tfull[acc], parity, abort);
             if (!__all_sync(0xffffffffu, ok)) break;
             vl_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kVlNMax;
@@ -610,21 +660,25 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
             const int rows = jb.kind == VL_DZ_T || jb.kind == VL_DZKL_T ? jb.pitch : jb.M;
             if (x.m0 + (int)rank * 128 + q * 32 < rows) {
                 switch (jb.kind) {
-                case VL_LSE: vl_epi_lse(jb, x, row, taddr); break;
-                case VL_DZ: vl_epi_dz(jb, x, row, taddr, prm.err); break;
-                case VL_DZKL: vl_epi_dzkl(jb, x, row, taddr); break;
-                case VL_DH: vl_epi_dh(jb, x, row, taddr); break;
-                case VL_DW: vl_epi_dw(jb, x, row, taddr); break;
-                case VL_LSE_T: vl_epi_lse_t(jb, row, taddr, lane); break;
-                case VL_DZ_T: vl_epi_dz_t(jb, sm, row, taddr); break;
-                case VL_DZKL_T: vl_epi_dzkl_t(jb, sm, row, taddr); break;
-                default: vl_epi_dh_t(jb, x, row, taddr); break;
+                case VL_LSE:
+                    ok = vl_epi_lse(jb, x, row, taddr, half, &tail.half[acc][q * 32 + lane], &sm.half[acc][q], parity, abort);
+                    break;
+                case VL_DZ: vl_epi_dz(jb, x, row, taddr, half, prm.err); break;
+                case VL_DZKL: vl_epi_dzkl(jb, x, row, taddr, half); break;
+                case VL_DH: vl_epi_dh(jb, x, row, taddr, half); break;
+                case VL_DW: vl_epi_dw(jb, x, row - lane, lane, taddr, half, smem_u32(tail.store[warp - 4])); break;
+                case VL_LSE_T: vl_epi_lse_t(jb, row, taddr, half, lane); break;
+                case VL_DZ_T: vl_epi_dz_t(jb, tail, row, taddr, half); break;
+                case VL_DZKL_T: vl_epi_dzkl_t(jb, tail, row, taddr, half); break;
+                default: vl_epi_dh_t(jb, x, row, taddr, half); break;
                 }
             }
+            if (!ok) break;
             vl_fence_before();
             __syncwarp();
             if (lane == 0) vl_arrive_at(acc ? free1 : free0);
         }
+        if (jb.kind == VL_DW) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
     }
 
     vl_fence_before();
@@ -705,7 +759,7 @@ static cudaError_t vl_launch(VlParams &p, cudaStream_t s)
     p.pairs = (int)std::min<long>(kVlPairs, (long)j.mt * j.nt * j.splits);
     p.stage_bytes = kVlABytes + (uint32_t)j.bn / 2 * kVlK * 2;
     p.stages = (int)std::min<uint32_t>(kVlStages, kVlRing / p.stage_bytes);
-    const size_t smem = 1024 + kVlRing;
+    const size_t smem = 1024 + kVlShared;
     cudaError_t e = cudaFuncSetAttribute(vocab_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -796,13 +850,14 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const int zbn = pl.z_narrow ? vl_narrow_bn(pl.zrows) : kVlNMax, hbn = pl.h_narrow ? vl_narrow_bn(N) : kVlNMax;
     // zh: hidden rows, zw: head rows (both along k); dzk: dz along its ids; wm:
-    // head columns; dzm, hm: dz's and h's columns (dW)
-    CUtensorMap zh, zw, dzk, dzm, wm, hm;
+    // head columns; dzm, hm: dz's and h's columns (dW); dwm: dW itself
+    CUtensorMap zh, zw, dzk, dzm, wm, hm, dwm;
     const bool ok = make_tmap_box(&zh, a.kl ? (const void *)hx : a.h, pl.zrows, d, 64, pl.z_narrow ? zbn / 2 : 128) &&
                     make_tmap_box(&zw, a.w, a.V, d, 64, 128) &&
                     make_tmap_box(&dzk, dz, N, pl.piece, 64, pl.h_narrow ? hbn / 2 : 128) &&
                     make_tmap_box(&wm, a.w, a.V, d, 64, kVlK) &&
-                    (!a.dw || (make_tmap_box(&dzm, dz, N, pl.piece, 64, kVlK) && make_tmap_box(&hm, hx, N, d, 64, kVlK)));
+                    (!a.dw || (make_tmap_box(&dzm, dz, N, pl.piece, 64, kVlK) && make_tmap_box(&hm, hx, N, d, 64, kVlK) &&
+                                make_tmap_box(&dwm, a.dw, a.V, d, 64, 32)));
     if (!ok) return cudaErrorInvalidValue;
     VlParams p;
     for (int v0 = 0; v0 < a.V; v0 += pl.piece) {
@@ -841,8 +896,8 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
             j.kind = VL_DW; j.M = nv; j.N = d; j.chunks = (N + kVlK - 1) / kVlK; j.splits = 1;
             j.bn = 256; j.mt = (nv + kVlM - 1) / kVlM; j.nt = (d + 255) / 256; j.n_fast = 1;
             j.a_mn = j.b_mn = 1;
-            j.out = (bf16 *)a.dw + (size_t)v0 * d;
-            j.a = dzm; j.b = hm;
+            j.c_off = v0;
+            j.a = dzm; j.b = hm; j.c = dwm;
             p.err = a.err;
             if ((e = vl_launch(p, s)) != cudaSuccess) return e;
         }
