@@ -64,6 +64,7 @@ struct VlJob {
     int kind;
     int M, N;            // valid rows and columns of the result
     int chunks, splits;  // k chunks of kVlK, and the shares they are cut into (DH)
+    int kr;              // k of a chunk that are loaded and multiplied: kVlK, or fewer (DW of few rows)
     int bn, mt, nt;
     int a_mn, b_mn;      // operand order in memory: 1 = MN-major
     int a_off, b_off;    // first row (K-major) or k row (MN-major): the piece's offset in W
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
             for (int t = pair; t < tiles && !stop; t += prm.pairs) {
                 const VlTile x = vl_tile(jb, t);
                 const int am = x.m0 + (int)rank * 128, bnh = jb.bn / 2, bx = x.n0 + (int)rank * bnh;
-                const uint32_t bytes = 2 * (kVlABytes + (uint32_t)bnh * kVlK * 2);
+                const uint32_t bytes = 2 * (128 + (uint32_t)bnh) * jb.kr * 2;
                 for (int i = 0; i < x.nc; ++i) {
                     if (!vl_wait(&sm.empty[stage], phase ^ 1, abort) || *abort) { stop = true; break; }
                     if (rank == 0) vl_expect_tx(&sm.full[stage], bytes);
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
                     const uint64_t ad = a_mn ? vl_desc_mn(a) : vl_desc_k(a), bd = b_mn ? vl_desc_mn(b) : vl_desc_k(b);
 #pragma unroll
                     for (int k = 0; k < kVlK / 16; ++k)
-                        vl_mma(d, ad + as * (k & 3) + ah * (k >> 2), bd + bs * (k & 3) + bh * (k >> 2), idesc,
+                        if (k * 16 < jb.kr) vl_mma(d, ad + as * (k & 3) + ah * (k >> 2), bd + bs * (k & 3) + bh * (k >> 2), idesc,
                                (i > 0 || k > 0) ? 1u : 0u);
                     vl_commit(&sm.empty[stage]);
                     if (++stage == (uint32_t)prm.stages) { stage = 0; phase ^= 1; }
@@ -794,6 +795,7 @@ cudaError_t loss_fwd_tc(const LossArgs &a, cudaStream_t s)
     VlParams p;
     memset(&p, 0, sizeof(p));
     VlJob &j = p.job;
+    j.kr = kVlK;
     const bool narrow = vl_narrow(a.N);
     const int rows = narrow ? a.V : a.N, cols = narrow ? a.N : a.V;
     j.kind = narrow ? VL_LSE_T : VL_LSE; j.M = rows; j.N = cols; j.chunks = (a.d + kVlK - 1) / kVlK; j.splits = 1;
@@ -849,6 +851,7 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
         e = launch_k(vl_clean_kernel, N, 256, 0, s, (const uint4 *)a.h, a.targets, a.g, a.V, (uint4 *)hx, d / 8);
     if (e != cudaSuccess) return e;
     const int zbn = pl.z_narrow ? vl_narrow_bn(pl.zrows) : kVlNMax, hbn = pl.h_narrow ? vl_narrow_bn(N) : kVlNMax;
+    const int wk = (int)std::min<size_t>(kVlK, up(N, 16));   // k of dW's chunks
     // zh: hidden rows, zw: head rows (both along k); dzk: dz along its ids; wm:
     // head columns; dzm, hm: dz's and h's columns (dW); dwm: dW itself
     CUtensorMap zh, zw, dzk, dzm, wm, hm, dwm;
@@ -856,7 +859,7 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
                     make_tmap_box(&zw, a.w, a.V, d, 64, 128) &&
                     make_tmap_box(&dzk, dz, N, pl.piece, 64, pl.h_narrow ? hbn / 2 : 128) &&
                     make_tmap_box(&wm, a.w, a.V, d, 64, kVlK) &&
-                    (!a.dw || (make_tmap_box(&dzm, dz, N, pl.piece, 64, kVlK) && make_tmap_box(&hm, hx, N, d, 64, kVlK) &&
+                    (!a.dw || (make_tmap_box(&dzm, dz, N, pl.piece, 64, wk) && make_tmap_box(&hm, hx, N, d, 64, wk) &&
                                 make_tmap_box(&dwm, a.dw, a.V, d, 64, 32)));
     if (!ok) return cudaErrorInvalidValue;
     VlParams p;
@@ -865,6 +868,7 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
         {
             memset(&p, 0, sizeof(p));
             VlJob &j = p.job;
+            j.kr = kVlK;
             j.kind = a.kl ? (pl.z_narrow ? VL_DZKL_T : VL_DZKL) : (pl.z_narrow ? VL_DZ_T : VL_DZ);
             j.M = pl.z_narrow ? nv : pl.zrows; j.N = pl.z_narrow ? pl.zrows : nv;
             j.chunks = (d + kVlK - 1) / kVlK; j.splits = 1; j.bn = zbn;
@@ -879,6 +883,7 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
         {
             memset(&p, 0, sizeof(p));
             VlJob &j = p.job;
+            j.kr = kVlK;
             j.kind = pl.h_narrow ? VL_DH_T : VL_DH;
             j.M = pl.h_narrow ? d : N; j.N = pl.h_narrow ? N : d; j.chunks = (nv + kVlK - 1) / kVlK;
             j.splits = std::min(pl.splits, j.chunks);
@@ -893,8 +898,9 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
         if (a.dw) {
             memset(&p, 0, sizeof(p));
             VlJob &j = p.job;
+            j.kr = kVlK;
             j.kind = VL_DW; j.M = nv; j.N = d; j.chunks = (N + kVlK - 1) / kVlK; j.splits = 1;
-            j.bn = 256; j.mt = (nv + kVlM - 1) / kVlM; j.nt = (d + 255) / 256; j.n_fast = 1;
+            j.bn = 256; j.mt = (nv + kVlM - 1) / kVlM; j.nt = (d + 255) / 256; j.n_fast = 1; j.kr = wk;
             j.a_mn = j.b_mn = 1;
             j.c_off = v0;
             j.a = dzm; j.b = hm; j.c = dwm;
