@@ -649,11 +649,11 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
         const uint32_t free0 = vl_mapa(smem_u32(&sm.tempty[0]), 0), free1 = vl_mapa(smem_u32(&sm.tempty[1]), 0);
         const int half = (warp - 4) >> 2;
         int local = 0;
+        uint32_t halves = 0;   // phases of sm.half: they count the tiles that this quarter has rows in
         for (int t = pair; t < tiles; t += prm.pairs, ++local) {
             const VlTile x = vl_tile(jb, t);
             const int acc = local & 1, row = x.m0 + r;
-            const uint32_t parity = (local >> 1) & 1;
-            bool ok = vl_wait(&sm.tfull[acc], parity, abort);
+            bool ok = vl_wait(&sm.tfull[acc], (local >> 1) & 1, abort);
             if (!__all_sync(0xffffffffu, ok)) break;
             vl_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + acc * kVlNMax;
@@ -662,7 +662,8 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
             if (x.m0 + (int)rank * 128 + q * 32 < rows) {
                 switch (jb.kind) {
                 case VL_LSE:
-                    ok = vl_epi_lse(jb, x, row, taddr, half, &tail.half[acc][q * 32 + lane], &sm.half[acc][q], parity, abort);
+                    ok = vl_epi_lse(jb, x, row, taddr, half, &tail.half[acc][q * 32 + lane], &sm.half[acc][q], halves >> acc & 1, abort);
+                    halves ^= 1u << acc;
                     break;
                 case VL_DZ: vl_epi_dz(jb, x, row, taddr, half, prm.err); break;
                 case VL_DZKL: vl_epi_dzkl(jb, x, row, taddr, half); break;

@@ -516,6 +516,76 @@ def test_losses_full_vocabulary_rows():
     assert float(rel.max()) < 3 * half(BF)
 
 
+def test_losses_in_several_pieces():
+    """So many rows that the vocabulary is gone over in pieces, with a ragged
+    last piece: every element."""
+    n, d, V = 4000, 72, 20001
+    test_ce_lm_head(BF, n, d, V)
+    test_ce_lm_head_grad(BF, n, d, V)
+    test_kl_lm_head_grad(BF, n, d, V)
+
+
+def test_offsets_past_32_bits():
+    """A head and a table of more than 2^31 elements: the last ids' rows."""
+    n, d, V = 3, 4104, 530000
+    assert V * d > 1 << 31
+    g = gen(40)
+    w = torch.empty((V, d), dtype=BF, device=DEV).normal_(0.0, 0.03, generator=g)
+    h = normal(g, (n, d), BF)
+    t = torch.tensor([V - 1, 7, V - 3], dtype=torch.int32, device=DEV)
+    up = torch.tensor([0.5, -1.0, 2.0], device=DEV)
+    loss, lse = pkg.orthrus_ce_lm_head(h, w, t)
+    dh, dw = pkg.orthrus_ce_lm_head_grad(h, w, t, lse, up)
+    h2 = (h.float() + normal(g, (n, d), F32, 0.5)).to(BF)
+    ld = pkg.orthrus_ce_lm_head(h2, w, t)[1]
+    dk = pkg.orthrus_kl_lm_head_grad(h, h2, w, lse, ld, up)
+    H, H2 = h.to(F64), h2.to(F64)
+    z = torch.cat([H @ c.to(F64).T for c in w.split(65536)], 1)
+    z2 = torch.cat([H2 @ c.to(F64).T for c in w.split(65536)], 1)
+    L = torch.logsumexp(z, 1)
+    # (the logits here are below 10: d roundings of sums of that size, twice)
+    assert float(z.abs().max()) < 16
+    assert float((lse.to(F64) - L).abs().max()) < 2 * d * U * 16
+    assert float((loss.to(F64) - (L - z.gather(1, t.long()[:, None])[:, 0])).abs().max()) < 4 * d * U * 16
+    p = torch.softmax(z, 1)
+    dz = p.scatter_add(1, t.long()[:, None], torch.full((n, 1), -1.0, dtype=F64, device=DEV)) * up.to(F64)[:, None]
+    dk_z = (torch.softmax(z2, 1) - p) * up.to(F64)[:, None]
+    for got, x in ((dh, dz), (dk, dk_z)):
+        want = sum(x[:, i:i + 65536] @ w[i:i + 65536].to(F64) for i in range(0, V, 65536))
+        assert float((got.to(F64) - want).norm() / want.norm()) < 2 * half(BF)
+    ids = torch.tensor([0, 7, 255, 256, 523265, V - 257, V - 3, V - 2, V - 1], device=DEV)
+    wantw = dz[:, ids].T @ H
+    assert float(((dw[ids].to(F64) - wantw).norm(dim=1) / wantw.norm(dim=1)).max()) < 3 * half(BF)
+    del dw
+    rows = pkg.orthrus_embed_rows(w, t, 2.0)
+    assert torch.equal(rows, 2.0 * w[t.long()].float())
+    gt = pkg.orthrus_embed_grad(rows, t, V, dtype=BF)
+    assert torch.equal(gt[t.long()], rows.to(BF)) and not bool(gt[: V - 3].view(-1)[-8 * d:].any())
+
+
+def test_two_calls_at_once():
+    """Losses on two streams at the same time: each as alone."""
+    a, b = _loss_case(600, 256, 30000, BF, seed=41), _loss_case(40, 512, 60000, BF, seed=42)
+    pkg_lse = [pkg.orthrus_ce_lm_head(*x[:3])[1] for x in (a, b)]
+
+    def one(x, lse):
+        h, w, t, up = x
+        return (*pkg.orthrus_ce_lm_head(h, w, t), *pkg.orthrus_ce_lm_head_grad(h, w, t, lse, up),
+                pkg.orthrus_embed_grad(h, t, w.shape[0]))
+
+    alone = [one(x, lse) for x, lse in zip((a, b), pkg_lse)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = []
+        for s, x, lse in zip(streams, (a, b), pkg_lse):
+            with torch.cuda.stream(s):
+                got.append(one(x, lse))
+        torch.cuda.synchronize()
+        for g, w in zip(got, alone):
+            assert all(torch.equal(i, j) for i, j in zip(g, w))
+
+
 def test_loss_gradients_against_differences():
     """Central differences of the losses themselves, fp32 path, and of the KL
     forward entry point's definition."""

@@ -152,3 +152,24 @@ def test_binding_refuses_host_tensors(pkg):
                  lambda: pkg.orthrus_kl_lm_head_grad(h, h, w, f, f, f)):
         with pytest.raises(TypeError, match="CUDA"):
             call()
+
+
+def test_binding_refuses_extents_past_31_bits(pkg):
+    """An extent that the C entry's int32 would cut short is an error."""
+    class Rows:
+        is_cuda, dtype, device = True, torch.int32, torch.device("cuda", 0)
+
+        def __init__(self, *shape):
+            self.shape = torch.Size(shape)
+
+        def is_contiguous(self):
+            return True
+
+    assert tuple(pkg._need_rows("ids", Rows((1 << 31) - 1), (torch.int32,), (None,))) == ((1 << 31) - 1,)
+    for shape in ((1 << 31,), ((1 << 32) + 5,)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            pkg._need_rows("ids", Rows(*shape), (torch.int32,), (None,))
+    with pytest.raises(ValueError):
+        pkg._need_rows("x", Rows(4, 8), (torch.int32,), (4,))
+    with pytest.raises(ValueError):
+        pkg._need_rows("x", Rows(4, 8), (torch.int32,), (4, 9))
