@@ -53,6 +53,42 @@ template <> struct RowVec<bf16, 8> {
     }
 };
 
+// A chunk of VEC elements as loaded, not yet converted.
+template <class T, int VEC> struct RawVec {
+    static constexpr int U = VEC * (int)sizeof(T) / 16;
+    uint4 u[U];
+    __device__ __forceinline__ void load(const T *p)
+    {
+#pragma unroll
+        for (int i = 0; i < U; ++i) u[i] = ((const uint4 *)p)[i];
+    }
+    __device__ __forceinline__ void zero()
+    {
+#pragma unroll
+        for (int i = 0; i < U; ++i) u[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float (&v)[VEC]) const
+    {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (sizeof(T) == 4) v[(i * 4 + k) % VEC] = __uint_as_float(w[k]);
+                else {
+                    v[(i * 8 + 2 * k) % VEC] = __uint_as_float(w[k] << 16);
+                    v[(i * 8 + 2 * k + 1) % VEC] = __uint_as_float(w[k] & 0xffff0000u);
+                }
+        }
+    }
+};
+template <class T> struct RawVec<T, 1> {
+    T u;
+    __device__ __forceinline__ void load(const T *p) { u = *p; }
+    __device__ __forceinline__ void zero() { u = from_f<T>(0.f); }
+    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = to_f<T>(u); }
+};
+
 // Zeros in [p, p + bytes) by the n threads t = 0 .. n - 1 (p and bytes even).
 __device__ __forceinline__ void zero_span(char *p, size_t bytes, size_t t, size_t n)
 {
@@ -431,8 +467,11 @@ __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const T *dout, con
                                                               int run_blocks, float scale, int accumulate, TG *dtable,
                                                               float *part, ZeroFill z)
 {
-    constexpr int J = VEC == 8 ? 1 : 4;      // column chunks of a thread
-    constexpr int U = VEC == 8 ? 8 : 4;      // rows in flight
+    constexpr int J = VEC == 8 ? 1 : 2;                       // column chunks of a thread
+    constexpr int U = VEC == 8 && sizeof(T) == 4 ? 8 : 16;    // rows in flight
+    // a thread's rows in flight, passed to a rolled loop (unrolled, the flushes
+    // are tens of KB of code that each block fetches once)
+    __shared__ RawVec<T, VEC> held[U][J][kRunThreads];
     extern __shared__ int run_smem[];
     int *st = run_smem, *si = run_smem + P;
     pdl_trigger();
@@ -482,21 +521,22 @@ __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const T *dout, con
     clear();
     int cur = st[0], begin = 0;
     for (int r0 = 0; r0 < n; r0 += U) {
-        float v[U][J][VEC];
+        RawVec<T, VEC> v[U][J];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 const int c = (c0 + j * kRunThreads + threadIdx.x) * VEC;
-                if (r0 + u < n && c < d && st[r0 + u] < vocab)
-                    RowVec<T, VEC>::load(dout + (size_t)si[r0 + u] * d + c, v[u][j]);
-                else
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) v[u][j][e] = 0.f;
+                if (r0 + u < n && c < d && st[r0 + u] < vocab) v[u][j].load(dout + (size_t)si[r0 + u] * d + c);
+                else v[u][j].zero();
             }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (r0 + u >= n) break;
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < J; ++j) held[u][j][threadIdx.x] = v[u][j];
+        const int m = min(U, n - r0);
+#pragma unroll 1
+        for (int u = 0; u < m; ++u) {
             const int t = st[r0 + u];
             if (t != cur) {
                 flush(cur, begin, r0 + u);
@@ -505,9 +545,12 @@ __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const T *dout, con
                 begin = r0 + u;
             }
 #pragma unroll
-            for (int j = 0; j < J; ++j)
+            for (int j = 0; j < J; ++j) {
+                float x[VEC];
+                held[u][j][threadIdx.x].get(x);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) acc[j][e] += v[u][j][e];
+                for (int e = 0; e < VEC; ++e) acc[j][e] += x[e];
+            }
         }
     }
     flush(cur, begin, n);
@@ -597,7 +640,7 @@ static cudaError_t run_sums(const EmbedGradArgs &a, const EmbedGradPlan &p, cons
 {
     float *part = (float *)(a.ws + p.o_part);
     const bool vec = rows_aligned(a.dout, a.d) && rows_aligned(a.dtable, a.d);
-    const int cols = vec ? 8 * kRunThreads : 4 * kRunThreads, slabs = (a.d + cols - 1) / cols;
+    const int cols = vec ? 8 * kRunThreads : 2 * kRunThreads, slabs = (a.d + cols - 1) / cols;
     const int run_blocks = p.pieces * slabs, fill_blocks = z.bits && z.begin < (size_t)a.vocab * a.d * sizeof(TG) ? 8 * 148 : 0;
     auto sum = [&](auto kernel) {
         return launch_k(kernel, run_blocks + fill_blocks, kRunThreads, (size_t)p.piece * 8, s, (const T *)a.dout, tok, idx,
@@ -820,42 +863,6 @@ cudaError_t launch_norm_rows(const NormArgs &a, cudaStream_t s)
 constexpr int kNgThreads = 512;
 constexpr int kNgMaxCols = 8192;     // longest row the register path holds
 constexpr int kNgBlocks = 2 * 148;   // blocks: two per SM
-
-// A chunk of VEC elements as loaded, not yet converted.
-template <class T, int VEC> struct RawVec {
-    static constexpr int U = VEC * (int)sizeof(T) / 16;
-    uint4 u[U];
-    __device__ __forceinline__ void load(const T *p)
-    {
-#pragma unroll
-        for (int i = 0; i < U; ++i) u[i] = ((const uint4 *)p)[i];
-    }
-    __device__ __forceinline__ void zero()
-    {
-#pragma unroll
-        for (int i = 0; i < U; ++i) u[i] = make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ void get(float (&v)[VEC]) const
-    {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (sizeof(T) == 4) v[(i * 4 + k) % VEC] = __uint_as_float(w[k]);
-                else {
-                    v[(i * 8 + 2 * k) % VEC] = __uint_as_float(w[k] << 16);
-                    v[(i * 8 + 2 * k + 1) % VEC] = __uint_as_float(w[k] & 0xffff0000u);
-                }
-        }
-    }
-};
-template <class T> struct RawVec<T, 1> {
-    T u;
-    __device__ __forceinline__ void load(const T *p) { u = *p; }
-    __device__ __forceinline__ void zero() { u = from_f<T>(0.f); }
-    __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = to_f<T>(u); }
-};
 
 template <class TX, class T, int VEC, int G, int J>
 __global__ void __launch_bounds__(kNgThreads, VEC == 8 && J == 1 ? 2 : 1)
