@@ -37,10 +37,58 @@ template <class T> struct Operand {
     size_t row_stride, k_stride;
     int rows;
     const unsigned char *live;
-    __device__ __forceinline__ float at(int r, size_t k) const
+};
+
+// One element to shared memory, zero when it is not there: fp32 by an
+// asynchronous copy, bf16 converted on the way.
+template <class T> __device__ __forceinline__ void st_put(float *dst, const T *src, const T *any, bool ok)
+{
+    if constexpr (sizeof(T) == 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(smem_u32(dst)), "l"(ok ? src : any), "r"(ok ? 4 : 0)
+                     : "memory");
+    else
+        *dst = ok ? to_f<T>(*src) : 0.f;
+}
+
+// A thread's elements of an operand's steps.  k contiguous in memory (K): one k
+// and every 8th row; 8 k x 4 rows per warp, whole 32-byte sectors, and a warp's
+// 32 stores into the transposed tile hit 32 banks.  Otherwise one row and every
+// 4th k, lanes along the rows.
+template <class T, bool K> struct StLoader {
+    const Operand<T> &op;
+    const T *p;          // first element of the next step
+    size_t stride, step, k, kmax;
+    int r, kk, left;     // left: rows from r on
+    __device__ __forceinline__ StLoader(const Operand<T> &o, int row0, size_t k0, size_t k1) : op(o), kmax(k1)
     {
-        return live && !live[k] ? 0.f : to_f<T>(p[r * row_stride + k * k_stride]);
+        const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
+        r = K ? (l >> 3) + 4 * (w >> 2) : threadIdx.x % kSt;
+        kk = K ? (l & 7) + 8 * (w & 3) : threadIdx.x / kSt;
+        k = k0 + kk;
+        left = o.rows - row0 - r;
+        p = o.p + (size_t)(row0 + r) * o.row_stride + k * o.k_stride;
+        stride = K ? 8 * o.row_stride : 4 * o.k_stride;
+        step = kStK * o.k_stride;
     }
+    __device__ __forceinline__ void load(float (&s)[kStK][kSt + 4])
+    {
+#pragma unroll
+        for (int q = 0; q < kStLoads; ++q) {
+            const bool ok = K ? 8 * q < left && k < kmax
+                              : left > 0 && k + 4 * q < kmax && !(op.live && !op.live[k + 4 * q]);
+            st_put(K ? &s[kk][r + 8 * q] : &s[kk + 4 * q][r], p + q * stride, op.p, ok);
+        }
+        p += step;
+        k += kStK;
+    }
+};
+static_assert(kStThreads == 8 * 32 && kSt == 64 && kStK == 32, "StLoader's cut of a step");
+
+union StSmem {
+    struct {
+        float a[2][kStK][kSt + 4], b[2][kStK][kSt + 4];   // two steps: one is loaded under the other's products
+    };
+    float z[kSt][kSt + 1];
 };
 
 // acc[i][j] = sum over k in [k0, k1) of A(m0 + 4 ty + i, k) B(n0 + 4 tx + j, k).
@@ -48,7 +96,7 @@ template <class T> struct Operand {
 // with the root of K / 128, not of K.  AK / BK: the operand's k is contiguous.
 template <class TA, class TB, bool AK, bool BK>
 __device__ void simt_tile(const Operand<TA> &A, const Operand<TB> &B, int m0, int n0, size_t k0, size_t k1,
-                          float (&acc)[4][4], float (&sa)[kStK][kSt + 4], float (&sb)[kStK][kSt + 4])
+                          float (&acc)[4][4], StSmem &sm)
 {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     float part[4][4];
@@ -56,31 +104,19 @@ __device__ void simt_tile(const Operand<TA> &A, const Operand<TB> &B, int m0, in
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) { acc[i][j] = 0.f; part[i][j] = 0.f; }
-    float ra[kStLoads], rb[kStLoads];
-    auto fetch = [&](size_t k) {
-#pragma unroll
-        for (int q = 0; q < kStLoads; ++q) {   // consecutive threads walk the contiguous axis
-            const int e = threadIdx.x + q * kStThreads;
-            const int ar = AK ? e / kStK : e % kSt, ak = AK ? e % kStK : e / kSt;
-            const int br = BK ? e / kStK : e % kSt, bk = BK ? e % kStK : e / kSt;
-            ra[q] = m0 + ar < A.rows && k + ak < k1 ? A.at(m0 + ar, k + ak) : 0.f;
-            rb[q] = n0 + br < B.rows && k + bk < k1 ? B.at(n0 + br, k + bk) : 0.f;
-        }
-    };
-    fetch(k0);
+    StLoader<TA, AK> la(A, m0, k0, k1);
+    StLoader<TB, BK> lb(B, n0, k0, k1);
+    if (k0 < k1) { la.load(sm.a[0]); lb.load(sm.b[0]); }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
     int step = 0;
     for (size_t k = k0; k < k1; k += kStK) {
-#pragma unroll
-        for (int q = 0; q < kStLoads; ++q) {
-            const int e = threadIdx.x + q * kStThreads;
-            if (AK) sa[e % kStK][e / kStK] = ra[q]; else sa[e / kSt][e % kSt] = ra[q];
-            if (BK) sb[e % kStK][e / kStK] = rb[q]; else sb[e / kSt][e % kSt] = rb[q];
-        }
+        const int buf = step & 1;
+        if (k + kStK < k1) { la.load(sm.a[buf ^ 1]); lb.load(sm.b[buf ^ 1]); }
+        asm volatile("cp.async.commit_group;\ncp.async.wait_group 1;\n" ::: "memory");
         __syncthreads();
-        if (k + kStK < k1) fetch(k + kStK);
 #pragma unroll
         for (int kk = 0; kk < kStK; ++kk) {
-            const float4 a = *(const float4 *)&sa[kk][ty * 4], b = *(const float4 *)&sb[kk][tx * 4];
+            const float4 a = *(const float4 *)&sm.a[buf][kk][ty * 4], b = *(const float4 *)&sm.b[buf][kk][tx * 4];
             const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -94,15 +130,12 @@ __device__ void simt_tile(const Operand<TA> &A, const Operand<TB> &B, int m0, in
 #pragma unroll
                 for (int j = 0; j < 4; ++j) { acc[i][j] += part[i][j]; part[i][j] = 0.f; }
     }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 }
 
 // The shift of a sum of exponentials whose maximum is m: 0 where every term is
 // exp(-inf) (a NaN among them still makes the sum a NaN).
 __device__ __forceinline__ float exp_shift(float m) { return m == -INFINITY ? 0.f : m; }
-
-struct StSmem {
-    float a[kStK][kSt + 4], b[kStK][kSt + 4];
-};
 
 // Forward: per (64-id tile, row) maximum and sum of exponentials, and the
 // logit of the row's target.
@@ -111,32 +144,31 @@ __global__ void __launch_bounds__(kStThreads) ce_tile_simt(const T *h, const T *
                                                            int V, float2 *rec, float *zt)
 {
     __shared__ __align__(16) StSmem sm;
-    __shared__ float z[kSt][kSt + 1];
-    pdl_trigger();
     pdl_wait();
     const int m0 = blockIdx.y * kSt, n0 = blockIdx.x * kSt;
     float acc[4][4];
     const Operand<T> A{h, (size_t)d, 1, N, nullptr}, B{w, (size_t)d, 1, V, nullptr};
-    simt_tile<T, T, true, true>(A, B, m0, n0, 0, d, acc, sm.a, sm.b);
+    simt_tile<T, T, true, true>(A, B, m0, n0, 0, d, acc, sm);
+    pdl_trigger();   // (late: blocks that wait for this kernel would crowd its own onto fewer SMs)
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) z[ty * 4 + i][tx * 4 + j] = acc[i][j];
+        for (int j = 0; j < 4; ++j) sm.z[ty * 4 + i][tx * 4 + j] = acc[i][j];
     __syncthreads();
     const int r = threadIdx.x >> 2, q = threadIdx.x & 3, row = m0 + r, nv = min(kSt, V - n0);
     float m = -INFINITY, s = 0.f;
-    for (int c = q; c < nv; c += 4) m = fmaxf(m, z[r][c]);
+    for (int c = q; c < nv; c += 4) m = fmaxf(m, sm.z[r][c]);
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const float sh = exp_shift(m);
-    for (int c = q; c < nv; c += 4) s += expf(z[r][c] - sh);
+    for (int c = q; c < nv; c += 4) s += expf(sm.z[r][c] - sh);
     s += __shfl_xor_sync(0xffffffffu, s, 1);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     if (q == 0 && row < N) {
         rec[(size_t)blockIdx.x * N + row] = make_float2(m, s);
         const int t = targets[row];
-        if (t >= n0 && t < n0 + nv) zt[row] = z[r][t - n0];
+        if (t >= n0 && t < n0 + nv) zt[row] = sm.z[r][t - n0];
     }
 }
 
@@ -240,18 +272,18 @@ template <class T, bool KL>
 __global__ void __launch_bounds__(kStThreads) dz_tile_simt(LossArgs a, int v0, int Vp, float *dz, unsigned char *alive)
 {
     __shared__ __align__(16) StSmem sm;
-    pdl_trigger();
     pdl_wait();
     const int m0 = blockIdx.y * kSt, n0 = v0 + blockIdx.x * kSt, d = a.d;
     const int vend = min(a.V, v0 + Vp);
     float z[4][4], z2[4][4];
     const Operand<T> A{(const T *)a.h, (size_t)d, 1, a.N, nullptr}, B{(const T *)a.w, (size_t)d, 1, a.V, nullptr};
-    simt_tile<T, T, true, true>(A, B, m0, n0, 0, d, z, sm.a, sm.b);
+    simt_tile<T, T, true, true>(A, B, m0, n0, 0, d, z, sm);
     if (KL) {
         const Operand<T> A2{(const T *)a.h2, (size_t)d, 1, a.N, nullptr};
-        simt_tile<T, T, true, true>(A2, B, m0, n0, 0, d, z2, sm.a, sm.b);
+        simt_tile<T, T, true, true>(A2, B, m0, n0, 0, d, z2, sm);
     }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    pdl_trigger();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = m0 + ty * 4 + i;
@@ -295,7 +327,8 @@ __device__ __forceinline__ void grad_tile(const Operand<TA> &A, const Operand<TB
     const size_t per = (((size_t)g.K + g.splits - 1) / g.splits + kStK - 1) / kStK * kStK;
     const size_t k0 = min((size_t)g.K, per * sp), k1 = min((size_t)g.K, k0 + per);
     float acc[4][4];
-    simt_tile<TA, TB, AK, false>(A, B, m0, n0, k0, k1, acc, sm.a, sm.b);
+    simt_tile<TA, TB, AK, false>(A, B, m0, n0, k0, k1, acc, sm);
+    pdl_trigger();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -323,7 +356,6 @@ __global__ void __launch_bounds__(kStThreads) grads_simt(Operand<float> dz, Oper
                                                          Operand<float> dzt, Operand<T> h, GradGemm gw)
 {
     __shared__ __align__(16) StSmem sm;
-    pdl_trigger();
     pdl_wait();
     if (blockIdx.x < h_blocks) grad_tile<float, T, true, T>(dz, w, gh, blockIdx.x, sm);
     else grad_tile<float, T, false, T>(dzt, h, gw, blockIdx.x - h_blocks, sm);
@@ -333,13 +365,13 @@ __global__ void __launch_bounds__(kStThreads) grads_simt(Operand<float> dz, Oper
 template <class T>
 __global__ void __launch_bounds__(256) part_sum_kernel(const float *part, int splits, size_t n, T *out)
 {
-    pdl_trigger();
     pdl_wait();
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) {
         float s = part[i];
         for (int k = 1; k < splits; ++k) s += part[(size_t)k * n + i];
         out[i] = from_f<T>(s);
     }
+    pdl_trigger();   // (late, as above: the next call's 64 blocks went to the 20 SMs that this kernel left free)
 }
 
 cudaError_t launch_part_sum(const float *part, int splits, size_t n, void *out, int dtype, cudaStream_t s)
