@@ -179,13 +179,15 @@ def _need(x, dtype, name):
 # Context-free mirrors: outputs and workspaces come from torch's allocator on
 # the tensors' device and that device's current stream.  `err` is an optional
 # int32 device tensor of one element that collects the ORTHRUS_DEVERR_* bits.
+_torch = None   # the module, imported by the first call
 _DT = None      # torch dtype -> orthrus_dtype_t
 
 
 def _dtypes():
-    global _DT
+    global _DT, _torch
     if _DT is None:
         import torch
+        _torch = torch
         _DT = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
     return _DT
 
@@ -218,16 +220,16 @@ def _need_rows(name, x, dtypes, shape, device=None):
 class _OnDevice:
     """The call's device made current for the launches, and its stream."""
 
+    __slots__ = ("index", "guard")
+
     def __init__(self, device):
-        import torch
         self.index = device.index
-        self.raw_stream = torch._C._cuda_getCurrentRawStream
-        self.guard = None if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
+        self.guard = None if _torch._C._cuda_getDevice() == device.index else _torch.cuda.device(device)
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        return self.raw_stream(self.index)
+        return _torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.guard is not None:
@@ -236,38 +238,35 @@ class _OnDevice:
 
 def _train_ws(name, device, *args):
     """Workspace of one call: (tensor, 256-byte aligned pointer, bytes)."""
-    import torch
     n = C.c_size_t()
     _check(name, getattr(lib(), name)(*args, C.byref(n)))
     if n.value == 0:
         return None, None, 0
-    ws = torch.empty(n.value + 256, dtype=torch.uint8, device=device)
-    return ws, C.c_void_p((ws.data_ptr() + 255) & ~255), n.value
+    ws = _torch.empty(n.value + 256, dtype=_torch.uint8, device=device)
+    return ws, (ws.data_ptr() + 255) & ~255, n.value
 
 
 def _err_ptr(err, device):
-    import torch
     if err is None:
         return None
-    _need_rows("err", err, (torch.int32,), (1,), device)
-    return _ptr(err)
+    _need_rows("err", err, (_torch.int32,), (1,), device)
+    return err.data_ptr()
 
 
 def orthrus_embed_rows(table, ids, scale=1.0, out_dtype=None, err=None):
     """scale * table[ids]: table [vocab, hidden] (bf16 or fp32), ids int32
     [rows] (negative: a zero row).  Returns [rows, hidden] of out_dtype (default
     fp32, the residual stream's)."""
-    import torch
     V, d = _need_rows("table", table, _dtypes(), (None, None))
     dev = table.device
-    n, = _need_rows("ids", ids, (torch.int32,), (None,), dev)
-    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    n, = _need_rows("ids", ids, (_torch.int32,), (None,), dev)
+    out_dtype = _torch.float32 if out_dtype is None else out_dtype
     od = _dtype_id("out_dtype", out_dtype)
     with _OnDevice(dev) as stream:
-        out = torch.empty((n, d), dtype=out_dtype, device=dev)
+        out = _torch.empty((n, d), dtype=out_dtype, device=dev)
         _check("orthrus_embed_rows", lib().orthrus_embed_rows(
-            _ptr(table), _dtype_id("table", table.dtype), V, d, _ptr(ids), n, float(scale), _ptr(out), od,
-            _err_ptr(err, dev), stream))
+            table.data_ptr(), _dtype_id("table", table.dtype), V, d, ids.data_ptr(), n, float(scale), out.data_ptr(),
+            od, _err_ptr(err, dev), stream))
     return out
 
 
@@ -275,11 +274,10 @@ def orthrus_embed_grad(dout, ids, vocab, scale=1.0, dtype=None, out=None, accumu
     """Gradient of orthrus_embed_rows in its table: [vocab, hidden] of `dtype`
     (default dout's), zeros for ids that do not occur.  With `out` the result is
     written there, or added to it when accumulate is set."""
-    import torch
     fl = _dtypes()
     n, d = _need_rows("dout", dout, fl, (None, None))
     dev = dout.device
-    _need_rows("ids", ids, (torch.int32,), (n,), dev)
+    _need_rows("ids", ids, (_torch.int32,), (n,), dev)
     vocab = int(vocab)
     if not 0 < vocab < 1 << 31:
         raise ValueError(f"vocab: expected 1 .. 2^31 - 1, got {vocab}")
@@ -289,44 +287,42 @@ def orthrus_embed_grad(dout, ids, vocab, scale=1.0, dtype=None, out=None, accumu
         _need_rows("out", out, fl if dtype is None else (dtype,), (vocab, d), dev)
     with _OnDevice(dev) as stream:
         if out is None:
-            out = torch.empty((vocab, d), dtype=dout.dtype if dtype is None else dtype, device=dev)
+            out = _torch.empty((vocab, d), dtype=dout.dtype if dtype is None else dtype, device=dev)
         od = _dtype_id("dtype", out.dtype)
         ws, wp, wn = _train_ws("orthrus_embed_grad_workspace", dev, n, d, vocab)
         _check("orthrus_embed_grad", lib().orthrus_embed_grad(
-            _ptr(dout), _dtype_id("dout", dout.dtype), _ptr(ids), n, d, vocab, float(scale), int(bool(accumulate)),
-            _ptr(out), od, wp, wn, _err_ptr(err, dev), stream))
+            dout.data_ptr(), _dtype_id("dout", dout.dtype), ids.data_ptr(), n, d, vocab, float(scale),
+            int(bool(accumulate)), out.data_ptr(), od, wp, wn, _err_ptr(err, dev), stream))
     return out
 
 
 def orthrus_rmsnorm(x, gain, eps):
     """x * gain / sqrt(mean(x^2) + eps) per row: x [rows, hidden] fp32 or gain's
     dtype; the result has gain's dtype."""
-    import torch
     n, d = _need_rows("x", x, _dtypes(), (None, None))
     _need_rows("gain", gain, _dtypes(), (d,), x.device)
     with _OnDevice(x.device) as stream:
-        y = torch.empty((n, d), dtype=gain.dtype, device=x.device)
+        y = _torch.empty((n, d), dtype=gain.dtype, device=x.device)
         _check("orthrus_rmsnorm", lib().orthrus_rmsnorm(
-            _ptr(x), _dtype_id("x", x.dtype), _ptr(gain), _dtype_id("gain", gain.dtype), n, d, float(eps), _ptr(y),
-            stream))
+            x.data_ptr(), _dtype_id("x", x.dtype), gain.data_ptr(), _dtype_id("gain", gain.dtype), n, d, float(eps),
+            y.data_ptr(), stream))
     return y
 
 
 def orthrus_rmsnorm_grad(x, gain, dy, eps):
     """Gradient of orthrus_rmsnorm: (dx [rows, hidden] of x's dtype, dgain fp32
     [hidden])."""
-    import torch
     n, d = _need_rows("x", x, _dtypes(), (None, None))
     dev = x.device
     _need_rows("gain", gain, _dtypes(), (d,), dev)
     _need_rows("dy", dy, (gain.dtype,), (n, d), dev)
     with _OnDevice(dev) as stream:
-        dx = torch.empty_like(x)
-        dgain = torch.empty(d, dtype=torch.float32, device=dev)
+        dx = _torch.empty_like(x)
+        dgain = _torch.empty(d, dtype=_torch.float32, device=dev)
         ws, wp, wn = _train_ws("orthrus_rmsnorm_grad_workspace", dev, n, d)
         _check("orthrus_rmsnorm_grad", lib().orthrus_rmsnorm_grad(
-            _ptr(x), _dtype_id("x", x.dtype), _ptr(gain), _ptr(dy), _dtype_id("gain", gain.dtype), n, d, float(eps),
-            _ptr(dx), _ptr(dgain), wp, wn, stream))
+            x.data_ptr(), _dtype_id("x", x.dtype), gain.data_ptr(), dy.data_ptr(), _dtype_id("gain", gain.dtype), n, d,
+            float(eps), dx.data_ptr(), dgain.data_ptr(), wp, wn, stream))
     return dx, dgain
 
 
@@ -334,39 +330,38 @@ def orthrus_ce_lm_head(h, w, targets, err=None):
     """Cross entropy through the LM head w [vocab, hidden] of the hidden rows h
     [rows, hidden] (same dtype): (loss, lse), fp32 [rows].  targets int32
     [rows]; negative: an ignored row (loss 0)."""
-    import torch
     n, d = _need_rows("h", h, _dtypes(), (None, None))
     dev = h.device
     V, _ = _need_rows("w", w, (h.dtype,), (None, d), dev)
-    _need_rows("targets", targets, (torch.int32,), (n,), dev)
+    _need_rows("targets", targets, (_torch.int32,), (n,), dev)
     dt = _dtype_id("h", h.dtype)
     with _OnDevice(dev) as stream:
-        loss = torch.empty(n, dtype=torch.float32, device=dev)
-        lse = torch.empty_like(loss)
+        loss = _torch.empty(n, dtype=_torch.float32, device=dev)
+        lse = _torch.empty_like(loss)
         ws, wp, wn = _train_ws("orthrus_ce_lm_head_workspace", dev, n, d, V, dt)
         _check("orthrus_ce_lm_head", lib().orthrus_ce_lm_head(
-            _ptr(h), _ptr(w), dt, _ptr(targets), n, d, V, _ptr(loss), _ptr(lse), wp, wn, _err_ptr(err, dev), stream))
+            h.data_ptr(), w.data_ptr(), dt, targets.data_ptr(), n, d, V, loss.data_ptr(), lse.data_ptr(), wp,
+            wn, _err_ptr(err, dev), stream))
     return loss, lse
 
 
 def orthrus_ce_lm_head_grad(h, w, targets, lse, dloss, weight_grad=True, err=None):
     """Gradient of orthrus_ce_lm_head from its lse and the upstream dloss (fp32
     [rows]): (dh [rows, hidden], dw [vocab, hidden] or None), h's dtype."""
-    import torch
     n, d = _need_rows("h", h, _dtypes(), (None, None))
     dev = h.device
     V, _ = _need_rows("w", w, (h.dtype,), (None, d), dev)
-    _need_rows("targets", targets, (torch.int32,), (n,), dev)
-    _need_rows("lse", lse, (torch.float32,), (n,), dev)
-    _need_rows("dloss", dloss, (torch.float32,), (n,), dev)
+    _need_rows("targets", targets, (_torch.int32,), (n,), dev)
+    _need_rows("lse", lse, (_torch.float32,), (n,), dev)
+    _need_rows("dloss", dloss, (_torch.float32,), (n,), dev)
     dt = _dtype_id("h", h.dtype)
     with _OnDevice(dev) as stream:
-        dh = torch.empty_like(h)
-        dw = torch.empty_like(w) if weight_grad else None
+        dh = _torch.empty_like(h)
+        dw = _torch.empty_like(w) if weight_grad else None
         ws, wp, wn = _train_ws("orthrus_ce_lm_head_grad_workspace", dev, n, d, V, dt, int(bool(weight_grad)))
         _check("orthrus_ce_lm_head_grad", lib().orthrus_ce_lm_head_grad(
-            _ptr(h), _ptr(w), dt, _ptr(targets), _ptr(lse), _ptr(dloss), n, d, V, _ptr(dh), _ptr(dw), wp, wn,
-            _err_ptr(err, dev), stream))
+            h.data_ptr(), w.data_ptr(), dt, targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), n, d, V,
+            dh.data_ptr(), None if dw is None else dw.data_ptr(), wp, wn, _err_ptr(err, dev), stream))
     return dh, dw
 
 
@@ -374,20 +369,19 @@ def orthrus_kl_lm_head_grad(h_ar, h_diff, w, lse_ar, lse_diff, dkl, err=None):
     """Gradient of the forward KL(softmax(w h_ar) || softmax(w h_diff)) in
     h_diff, from both log-sum-exps and the upstream dkl (fp32 [rows]): dh_diff
     [rows, hidden], h_diff's dtype."""
-    import torch
     n, d = _need_rows("h_ar", h_ar, _dtypes(), (None, None))
     dev = h_ar.device
     _need_rows("h_diff", h_diff, (h_ar.dtype,), (n, d), dev)
     V, _ = _need_rows("w", w, (h_ar.dtype,), (None, d), dev)
     for name, x in (("lse_ar", lse_ar), ("lse_diff", lse_diff), ("dkl", dkl)):
-        _need_rows(name, x, (torch.float32,), (n,), dev)
+        _need_rows(name, x, (_torch.float32,), (n,), dev)
     dt = _dtype_id("h_ar", h_ar.dtype)
     with _OnDevice(dev) as stream:
-        dh = torch.empty_like(h_diff)
+        dh = _torch.empty_like(h_diff)
         ws, wp, wn = _train_ws("orthrus_kl_lm_head_grad_workspace", dev, n, d, V, dt)
         _check("orthrus_kl_lm_head_grad", lib().orthrus_kl_lm_head_grad(
-            _ptr(h_ar), _ptr(h_diff), _ptr(w), dt, _ptr(lse_ar), _ptr(lse_diff), _ptr(dkl), n, d, V, _ptr(dh), wp, wn,
-            _err_ptr(err, dev), stream))
+            h_ar.data_ptr(), h_diff.data_ptr(), w.data_ptr(), dt, lse_ar.data_ptr(), lse_diff.data_ptr(),
+            dkl.data_ptr(), n, d, V, dh.data_ptr(), wp, wn, _err_ptr(err, dev), stream))
     return dh
 
 
