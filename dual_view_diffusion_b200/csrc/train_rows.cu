@@ -1,6 +1,8 @@
 // Row operators of the training side: the token embedding with scaling and
 // its gradient by sorted tokens, and RMSNorm with its gradient.  All of them
-// are bound by memory traffic (large calls) or launch latency (small ones).
+// are bound by memory traffic (large calls: 16384 embedded rows of 4096 in 73
+// us, 5.5 TB/s; the norm's gradient over 8192 rows of 4096 in 67 us, 5.0 TB/s)
+// or by the call itself (32 rows of 2048: 3.4 us of kernel in a 10 us call).
 #include <math.h>
 
 #include <algorithm>
@@ -209,7 +211,7 @@ __device__ __forceinline__ int sort_key(const int32_t *ids, int r, int vocab, un
 // written beside the sort, whoever they belong to, as many as the idle SMs
 // manage meanwhile; the rest beside the sums, by blocks that skip the rows
 // whose bit says that the token occurs (8192 rows of 4096, vocabulary 151936:
-// all zeros beside the sort, then the sums, 294 us; like this 243 us, of
+// all zeros beside the sort, then the sums, 294 us; like this 233 us, of
 // a floor of 204 us).
 struct ZeroFill {
     char *p;              // the table, or null (accumulating)
