@@ -1,7 +1,7 @@
 // Row operators of the training side: the token embedding with scaling and
 // its gradient by sorted tokens, and RMSNorm with its gradient.  All of them
-// are bound by memory traffic (large calls: 16384 embedded rows of 4096 in 73
-// us, 5.5 TB/s; the norm's gradient over 8192 rows of 4096 in 67 us, 5.0 TB/s)
+// are bound by memory traffic (large calls: 16384 embedded rows of 4096 in 63
+// us, 6.4 TB/s; the norm's gradient over 8192 rows of 4096 in 61 us, 5.5 TB/s)
 // or by the call itself (32 rows of 2048: 3.4 us of kernel in a 10 us call).
 #include <math.h>
 
@@ -13,8 +13,10 @@
 namespace orthrus {
 
 // ---------------------------------------------------------------- vectors
-// VEC elements of T as fp32: 16-byte accesses when VEC = 8 (two for fp32),
-// else one element at a time (odd row lengths, unaligned buffers).
+// VEC elements of T as fp32: 8 when all of a kernel's tensors are bf16 (16-byte
+// accesses), 4 when one is fp32 (16 bytes of it: with 8, two accesses of half
+// a sector each; 16384 embedded rows of 4096 took 73 us with 8, 63 with 4), 1
+// for odd row lengths and unaligned buffers.
 template <class T, int VEC> struct RowVec;
 template <class T> struct RowVec<T, 1> {
     static __device__ __forceinline__ void load(const T *p, float (&v)[1]) { v[0] = to_f<T>(*p); }
@@ -30,6 +32,30 @@ template <> struct RowVec<float, 8> {
     {
         ((float4 *)p)[0] = make_float4(v[0], v[1], v[2], v[3]);
         ((float4 *)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+};
+template <> struct RowVec<float, 4> {
+    static __device__ __forceinline__ void load(const float *p, float (&v)[4])
+    {
+        const float4 a = *(const float4 *)p;
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float (&v)[4])
+    {
+        *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]);
+    }
+};
+template <> struct RowVec<bf16, 4> {
+    static __device__ __forceinline__ void load(const bf16 *p, float (&v)[4])
+    {
+        const uint2 u = *(const uint2 *)p;
+        v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+        v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+    }
+    static __device__ __forceinline__ void store(bf16 *p, const float (&v)[4])
+    {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+        *(uint2 *)p = make_uint2(*(const uint32_t *)&a, *(const uint32_t *)&b);
     }
 };
 template <> struct RowVec<bf16, 8> {
@@ -84,6 +110,16 @@ template <class T, int VEC> struct RawVec {
         }
     }
 };
+template <> struct RawVec<bf16, 4> {
+    uint2 u;
+    __device__ __forceinline__ void load(const bf16 *p) { u = *(const uint2 *)p; }
+    __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
+    __device__ __forceinline__ void get(float (&v)[4]) const
+    {
+        v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+        v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+    }
+};
 template <class T> struct RawVec<T, 1> {
     T u;
     __device__ __forceinline__ void load(const T *p) { u = *p; }
@@ -112,7 +148,7 @@ template <class T, class TO, int VEC>
 __global__ void __launch_bounds__(kEmbThreads) embed_rows_kernel(const T *table, const int32_t *ids, TO *out, int d,
                                                                  int vocab, float scale, unsigned *err)
 {
-    constexpr int Q = 16 / VEC > 4 ? 4 : 16 / VEC;   // chunks of a thread in flight
+    constexpr int Q = VEC == 1 ? 4 : 16 / VEC;   // chunks of a thread in flight
     pdl_trigger();
     pdl_wait();
     const int row = blockIdx.x;
@@ -148,12 +184,13 @@ __global__ void __launch_bounds__(kEmbThreads) embed_rows_kernel(const T *table,
 template <class T, class TO> static cudaError_t embed_rows_t(const EmbedRowsArgs &a, cudaStream_t s)
 {
     const bool vec = rows_aligned(a.table, a.d) && rows_aligned(a.out, a.d);
-    const int per = vec ? 8 * 2 * kEmbThreads : 4 * kEmbThreads;   // elements a block covers per step
+    constexpr int V = sizeof(T) == 4 || sizeof(TO) == 4 ? 4 : 8;
+    const int per = (vec ? 16 : 4) * kEmbThreads;   // elements a block covers per step
     // one block per row and slab of the row, so that every element is in
     // flight at once; rows beyond 64 slabs loop
     const dim3 grid(a.rows, std::min(64, (a.d + per - 1) / per));
     if (vec)
-        return launch_k(embed_rows_kernel<T, TO, 8>, grid, kEmbThreads, 0, s, (const T *)a.table, a.ids, (TO *)a.out,
+        return launch_k(embed_rows_kernel<T, TO, V>, grid, kEmbThreads, 0, s, (const T *)a.table, a.ids, (TO *)a.out,
                         a.d, a.vocab, a.scale, a.err);
     return launch_k(embed_rows_kernel<T, TO, 1>, grid, kEmbThreads, 0, s, (const T *)a.table, a.ids, (TO *)a.out, a.d,
                     a.vocab, a.scale, a.err);
@@ -508,8 +545,7 @@ __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const T *dout, con
             if (c >= d) continue;
             if (head || tail) {
                 float *p = part + ((size_t)piece * 2 + (head ? 0 : 1)) * d + c;
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) p[q] = acc[j][q];
+                RowVec<float, VEC>::store(p, acc[j]);
             } else {
                 TG *o = dtable + (size_t)token * d + c;
                 float old[VEC], v[VEC];
@@ -838,11 +874,12 @@ template <class TX, class T> static cudaError_t norm_rows_t(const NormArgs &a, c
     };
     // threads per row: as few as hold it in registers, so that each has up to
     // four 16- or 32-byte loads in flight (8192 x 2048, fp32 x: 25.4 us with 256 threads a row, 14.4 us with 64)
+    constexpr int V = sizeof(T) == 4 ? 4 : 8;   // (only y is written: 8 bf16 of it are one access)
     if (vec)
-        return a.d <= 1024 ? go(norm_rows_kernel<TX, T, 8, 32>, 32)
-               : a.d <= 2048 ? go(norm_rows_kernel<TX, T, 8, 64>, 64)
-               : a.d <= 4096 ? go(norm_rows_kernel<TX, T, 8, 128>, 128)
-                             : go(norm_rows_kernel<TX, T, 8, 256>, 256);
+        return a.d <= 1024 ? go(norm_rows_kernel<TX, T, V, 32>, 32)
+               : a.d <= 2048 ? go(norm_rows_kernel<TX, T, V, 64>, 64)
+               : a.d <= 4096 ? go(norm_rows_kernel<TX, T, V, 128>, 128)
+                             : go(norm_rows_kernel<TX, T, V, 256>, 256);
     return a.d <= 256 ? go(norm_rows_kernel<TX, T, 1, 32>, 32) : go(norm_rows_kernel<TX, T, 1, 256>, 256);
 }
 
@@ -861,13 +898,14 @@ cudaError_t launch_norm_rows(const NormArgs &a, cudaStream_t s)
 // registers over all rows the block takes; each block leaves its column sums
 // in the workspace and a second kernel adds the blocks up in a fixed order.
 // The next row's loads are issued before this row's sums are joined, or the
-// memory would idle behind every row's barrier (8192 x 4096, fp32 x: 127.6 -> 67 us, of a floor of 52 us).
+// memory would idle behind every row's barrier (8192 x 4096, fp32 x: 128 us without, 70 with,
+// 61 with 4 fp32 per access, of a floor of 52 us).
 constexpr int kNgThreads = 512;
 constexpr int kNgMaxCols = 8192;     // longest row the register path holds
 constexpr int kNgBlocks = 2 * 148;   // blocks: two per SM
 
 template <class TX, class T, int VEC, int G, int J>
-__global__ void __launch_bounds__(kNgThreads, VEC == 8 && J == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kNgThreads, VEC * J == 8 ? 2 : 1)
     norm_grad_kernel(const TX *x, const T *gain, const T *dy, TX *dx, int rows, int d, float eps, float *part)
 {
     constexpr int R = kNgThreads / G;   // rows of a block at a time
@@ -951,9 +989,7 @@ __global__ void __launch_bounds__(kNgThreads, VEC == 8 && J == 1 ? 2 : 1)
                 for (int e = 0; e < VEC; ++e)
                     for (int q = 1; q < R; ++q) acc[j][e] += comb[(q * G + t) * VEC + e];
         }
-        if (gi == 0 && c < nc)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) p[(size_t)c * VEC + e] = acc[j][e];
+        if (gi == 0 && c < nc) RowVec<float, VEC>::store(p + (size_t)c * VEC, acc[j]);
     }
 }
 
@@ -1052,12 +1088,13 @@ template <class TX, class T> static cudaError_t norm_grad_t(const NormArgs &a, c
                             (TX *)a.out, a.rows, a.d, a.eps, part);
         };
         // threads per row: as few as hold the row in registers
+        constexpr int V = sizeof(TX) == 4 ? 4 : 8, J = 8 / V;
         if (vec)
-            e = a.d <= 256 ? go(norm_grad_kernel<TX, T, 8, 32, 1>, 32)
-                : a.d <= 1024 ? go(norm_grad_kernel<TX, T, 8, 128, 1>, 128)
-                : a.d <= 2048 ? go(norm_grad_kernel<TX, T, 8, 256, 1>, 256)
-                : a.d <= 4096 ? go(norm_grad_kernel<TX, T, 8, 512, 1>, 512)
-                              : go(norm_grad_kernel<TX, T, 8, 512, 2>, 512);
+            e = a.d <= 256 ? go(norm_grad_kernel<TX, T, V, 32, J>, 32)
+                : a.d <= 1024 ? go(norm_grad_kernel<TX, T, V, 128, J>, 128)
+                : a.d <= 2048 ? go(norm_grad_kernel<TX, T, V, 256, J>, 256)
+                : a.d <= 4096 ? go(norm_grad_kernel<TX, T, V, 512, J>, 512)
+                              : go(norm_grad_kernel<TX, T, V, 512, 2 * J>, 512);
         else
             e = a.d <= 512 ? go(norm_grad_kernel<TX, T, 1, 32, 16>, 32)
                 : a.d <= 2048 ? go(norm_grad_kernel<TX, T, 1, 128, 16>, 128)
