@@ -68,7 +68,7 @@ enum VlKind : int { VL_LSE = 0, VL_DZ = 1, VL_DZKL = 2, VL_DH = 3, VL_DW = 4, VL
 
 // The product of a launch: mt x nt x splits tiles; pair p takes tiles p, p + pairs, ..
 struct VlJob {
-    CUtensorMap a, b, c;   // c (DW): the result, boxes of 64 columns x 32 rows
+    CUtensorMap a, b, c;   // c (DZ, DZKL, DW): the result, boxes of 64 columns x a warp's rows
     int kind;
     int M, N;            // valid rows and columns of the result
     int chunks, splits;  // k chunks of kVlK, and the shares they are cut into (DH)
@@ -82,7 +82,7 @@ struct VlJob {
     const float *lse, *lse2, *g;
     float2 *rec;         // LSE: [nt][M]; LSE_T: [groups of 32 ids][N]
     float *zt;           // LSE: the rows' target logits
-    bf16 *dz;            // DZ: [rows][pitch]
+    bf16 *dz;            // DZ_T: [rows][pitch]
     int v0, V, pitch;    // DZ: the piece's first id, the vocabulary, dz's row length
     float *part;         // DH: [splits][M][N] fp32
     int add, last;       // DH: add to part; the last piece of an unsplit dh: write out
@@ -242,7 +242,7 @@ struct VlSmem {
 };
 // Behind the ring: LSE, the second warps' (maximum, sum) of a tile, per
 // accumulator; the transposed kinds, per column (row of h) lse * log2 e,
-// upstream gradient and target; DW, 4 KiB per epilogue warp.
+// upstream gradient and target; DZ, DZKL and DW, 4 KiB per epilogue warp.
 union VlTail {
     float2 half[2][128];
     struct {
@@ -304,14 +304,33 @@ __device__ __forceinline__ bool vl_epi_lse(const VlJob &jb, const VlTile &x, int
     return true;
 }
 
-// 16 bf16 columns of a row of dz
-__device__ __forceinline__ void vl_store16(bf16 *p, const float (&v)[16])
+// Results in bf16 leave by TMA, a box of 64 columns at a time through the warp's
+// 4 KiB of shared memory (rows of 128 bytes, 128-byte swizzle): whole lines
+// (16-byte stores of a row per thread took about 310 us for the dW of 31 rows of
+// 2048, vocabulary 151936; the boxes take 170 us).  The map clips what lies past
+// the last row or column.
+//
+// the buffer is free again (lane 0 issued the copies; a warp sync follows)
+__device__ __forceinline__ void vl_box_free() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+// eight columns of a row: 16-byte piece `piece` of its 128 bytes
+__device__ __forceinline__ void vl_box_put(uint32_t buf, int row, int piece, const float *v)
 {
-    ((uint4 *)p)[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    ((uint4 *)p)[1] = make_uint4(pack_bf16(v[8], v[9]), pack_bf16(v[10], v[11]), pack_bf16(v[12], v[13]), pack_bf16(v[14], v[15]));
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(buf + row * 128 + ((piece ^ (row & 7)) << 4)),
+                 "r"(pack_bf16(v[0], v[1])), "r"(pack_bf16(v[2], v[3])), "r"(pack_bf16(v[4], v[5])), "r"(pack_bf16(v[6], v[7]))
+                 : "memory");
+}
+__device__ __forceinline__ void vl_box_send(const CUtensorMap *map, int x, int y, uint32_t buf, int lane)
+{
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    __syncwarp();
+    if (lane == 0)
+        asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n"
+                     "cp.async.bulk.commit_group;\n" ::"l"((uint64_t)map), "r"(x), "r"(y), "r"(buf)
+                     : "memory");
 }
 
-__device__ __forceinline__ void vl_epi_dz(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, int half, unsigned *err)
+__device__ __forceinline__ void vl_epi_dz(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, int half, int lane,
+                                          uint32_t buf, unsigned *err)
 {
     float g = 0.f, k = 0.f;
     int t = -1;
@@ -323,50 +342,56 @@ __device__ __forceinline__ void vl_epi_dz(const VlJob &jb, const VlTile &x, int 
     }
     const int nv = jb.N - x.n0;                        // columns of the tile below the piece's end (may exceed bn)
     const int nc = min(jb.bn, jb.pitch - x.n0);        // columns dz has room for
-    bf16 *dst = jb.dz + (size_t)row * jb.pitch + x.n0;
-    for (int c = 32 * half; c < nc; c += 64) {
-        float r[32];
-        vl_tmem_ld32(taddr + c, r);
-        if (row >= jb.M) continue;
+    for (int c = 64 * half; c < nc; c += 128) {
+        vl_box_free();
 #pragma unroll
-        for (int h = 0; h < 32; h += 16) {
-            float v[16];
+        for (int q = 0; q < 64; q += 32) {
+            float r[32];
+            vl_tmem_ld32(taddr + c + q, r);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                float e = vl_exp2(fmaf(r[h + i], kLog2e, -k));
-                if (c + h + i == t) e -= 1.f;
+            for (int i = 0; i < 32; ++i) {
+                float e = vl_exp2(fmaf(r[i], kLog2e, -k));
+                if (c + q + i == t) e -= 1.f;
                 // rows without a share and columns past the vocabulary are exact zeros
-                v[i] = g == 0.f || c + h + i >= nv ? 0.f : g * e;
+                r[i] = g == 0.f || c + q + i >= nv ? 0.f : g * e;
             }
-            vl_store16(dst + c + h, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vl_box_put(buf, lane, q / 8 + i, r + 8 * i);
         }
+        vl_box_send(&jb.c, x.n0 + c, row - lane, buf, lane);
     }
 }
 
 // Interleaved rows: even lanes hold the AR view's logits of a position, odd
 // lanes the diffusion view's.  Each pair of lanes exchanges halves of a chunk
-// and writes 16 columns per lane.
-__device__ __forceinline__ void vl_epi_dzkl(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, int half)
+// and puts 16 columns per lane.
+__device__ __forceinline__ void vl_epi_dzkl(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, int half, int lane,
+                                            uint32_t buf)
 {
     const int pos = row >> 1, odd = row & 1;
     const bool live = row < jb.M;
     const float k = live ? (odd ? jb.lse2 : jb.lse)[pos] * kLog2e : 0.f, g = live ? jb.g[pos] : 0.f;
     const int nv = jb.N - x.n0;
     const int nc = min(jb.bn, jb.pitch - x.n0);
-    bf16 *dst = jb.dz + (size_t)pos * jb.pitch + x.n0 + 16 * odd;
-    for (int c = 32 * half; c < nc; c += 64) {
-        float r[32], v[16];
-        vl_tmem_ld32(taddr + c, r);
+    for (int c = 64 * half; c < nc; c += 128) {
+        vl_box_free();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) r[i] = vl_exp2(fmaf(r[i], kLog2e, -k));
+        for (int q = 0; q < 64; q += 32) {
+            float r[32], v[16];
+            vl_tmem_ld32(taddr + c + q, r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float mine = odd ? r[16 + i] : r[i];
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? r[i] : r[16 + i], 1);
-            const float e = odd ? mine - other : other - mine;   // p_diff - p_AR
-            v[i] = g == 0.f || c + 16 * odd + i >= nv ? 0.f : g * e;
+            for (int i = 0; i < 32; ++i) r[i] = vl_exp2(fmaf(r[i], kLog2e, -k));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float mine = odd ? r[16 + i] : r[i];
+                const float other = __shfl_xor_sync(0xffffffffu, odd ? r[i] : r[16 + i], 1);
+                const float e = odd ? mine - other : other - mine;   // p_diff - p_AR
+                v[i] = g == 0.f || c + q + 16 * odd + i >= nv ? 0.f : g * e;
+            }
+            vl_box_put(buf, lane >> 1, q / 8 + 2 * odd, v);
+            vl_box_put(buf, lane >> 1, q / 8 + 2 * odd + 1, v + 8);
         }
-        if (live) vl_store16(dst + c, v);
+        vl_box_send(&jb.c, x.n0 + c, (row - lane) >> 1, buf, lane);
     }
 }
 
@@ -398,35 +423,20 @@ __device__ __forceinline__ void vl_epi_dh(const VlJob &jb, const VlTile &x, int 
     }
 }
 
-// dW leaves by TMA: 64 columns x 32 rows at a time through shared memory, whole
-// 128-byte lines (16-byte stores of a row per thread took about 310 us for the dW of
-// 31 rows of 2048, vocabulary 151936; this takes 170 us).  The map clips what lies
-// past the last row or column.
-__device__ __forceinline__ void vl_epi_dw(const VlJob &jb, const VlTile &x, int row0, int lane, uint32_t taddr,
-                                          int half, uint32_t buf)
+__device__ __forceinline__ void vl_epi_dw(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, int half, int lane,
+                                          uint32_t buf)
 {
     const int nv = min(jb.bn, jb.N - x.n0);
-    const uint32_t dst = buf + lane * 128;
     for (int c = 64 * half; c < nv; c += 128) {
-        asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+        vl_box_free();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int q = 0; q < 64; q += 32) {
             float r[32];
-            vl_tmem_ld32(taddr + c + 32 * h, r);   // (its warp sync orders lane 0's wait before the stores)
+            vl_tmem_ld32(taddr + c + q, r);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(dst + (((4 * h + i) ^ (lane & 7)) << 4)),
-                             "r"(pack_bf16(r[8 * i], r[8 * i + 1])), "r"(pack_bf16(r[8 * i + 2], r[8 * i + 3])),
-                             "r"(pack_bf16(r[8 * i + 4], r[8 * i + 5])), "r"(pack_bf16(r[8 * i + 6], r[8 * i + 7]))
-                             : "memory");
+            for (int i = 0; i < 4; ++i) vl_box_put(buf, lane, q / 8 + i, r + 8 * i);
         }
-        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n"
-                         "cp.async.bulk.commit_group;\n" ::"l"((uint64_t)&jb.c), "r"(x.n0 + c), "r"(jb.c_off + row0), "r"(dst)
-                         : "memory");
-        }
+        vl_box_send(&jb.c, x.n0 + c, jb.c_off + row - lane, buf, lane);
     }
 }
 
@@ -656,6 +666,7 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
         const int r = (int)rank * 128 + q * 32 + lane;   // row in the tile
         const uint32_t free0 = vl_mapa(smem_u32(&sm.tempty[0]), 0), free1 = vl_mapa(smem_u32(&sm.tempty[1]), 0);
         const int half = (warp - 4) >> 2;
+        const uint32_t buf = smem_u32(tail.store[warp - 4]);
         int local = 0;
         uint32_t halves = 0;   // phases of sm.half: they count the tiles that this quarter has rows in
         for (int t = pair; t < tiles; t += prm.pairs, ++local) {
@@ -673,10 +684,10 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
                     ok = vl_epi_lse(jb, x, row, taddr, half, &tail.half[acc][q * 32 + lane], &sm.half[acc][q], halves >> acc & 1, abort);
                     halves ^= 1u << acc;
                     break;
-                case VL_DZ: vl_epi_dz(jb, x, row, taddr, half, prm.err); break;
-                case VL_DZKL: vl_epi_dzkl(jb, x, row, taddr, half); break;
+                case VL_DZ: vl_epi_dz(jb, x, row, taddr, half, lane, buf, prm.err); break;
+                case VL_DZKL: vl_epi_dzkl(jb, x, row, taddr, half, lane, buf); break;
                 case VL_DH: vl_epi_dh(jb, x, row, taddr, half); break;
-                case VL_DW: vl_epi_dw(jb, x, row - lane, lane, taddr, half, smem_u32(tail.store[warp - 4])); break;
+                case VL_DW: vl_epi_dw(jb, x, row, taddr, half, lane, buf); break;
                 case VL_LSE_T: vl_epi_lse_t(jb, row, taddr, half, lane); break;
                 case VL_DZ_T: vl_epi_dz_t(jb, tail, row, taddr, half); break;
                 case VL_DZKL_T: vl_epi_dzkl_t(jb, tail, row, taddr, half); break;
@@ -688,7 +699,7 @@ __global__ void __launch_bounds__(kVlThreads, 1) vocab_pair_kernel(const __grid_
             __syncwarp();
             if (lane == 0) vl_arrive_at(acc ? free1 : free0);
         }
-        if (jb.kind == VL_DW) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+        asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
     }
 
     vl_fence_before();
@@ -864,11 +875,12 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const int zbn = pl.z_narrow ? vl_narrow_bn(pl.zrows) : kVlNMax, hbn = pl.h_narrow ? vl_narrow_bn(N) : kVlNMax;
     const int wk = (int)std::min<size_t>(kVlK, up(N, 16));   // k of dW's chunks
-    // zh: hidden rows, zw: head rows (both along k); dzk: dz along its ids; wm:
+    // zh: hidden rows, zw: head rows (both along k); dzs: dz as it is written, dzk: dz along its ids; wm:
     // head columns; dzm, hm: dz's and h's columns (dW); dwm: dW itself
-    CUtensorMap zh, zw, dzk, dzm, wm, hm, dwm;
+    CUtensorMap zh, zw, dzs, dzk, dzm, wm, hm, dwm;
     const bool ok = make_tmap_box(&zh, a.kl ? (const void *)hx : a.h, pl.zrows, d, 64, pl.z_narrow ? zbn / 2 : 128) &&
                     make_tmap_box(&zw, a.w, a.V, d, 64, 128) &&
+                    make_tmap_box(&dzs, dz, N, pl.piece, 64, a.kl ? 16 : 32) &&
                     make_tmap_box(&dzk, dz, N, pl.piece, 64, pl.h_narrow ? hbn / 2 : 128) &&
                     make_tmap_box(&wm, a.w, a.V, d, 64, kVlK) &&
                     (!a.dw || (make_tmap_box(&dzm, dz, N, pl.piece, 64, wk) && make_tmap_box(&hm, hx, N, d, 64, wk) &&
@@ -888,7 +900,7 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
             (pl.z_narrow ? j.a_off : j.b_off) = v0;
             j.targets = a.targets; j.lse = a.lse_in; j.lse2 = a.lse2_in; j.g = a.g;
             j.dz = dz; j.v0 = v0; j.V = a.V; j.pitch = pl.piece;
-            j.a = pl.z_narrow ? zw : zh; j.b = pl.z_narrow ? zh : zw;
+            j.a = pl.z_narrow ? zw : zh; j.b = pl.z_narrow ? zh : zw; j.c = dzs;
             p.err = a.err;
             if ((e = vl_launch(p, s)) != cudaSuccess) return e;
         }
