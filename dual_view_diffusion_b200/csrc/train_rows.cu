@@ -681,6 +681,10 @@ static cudaError_t run_sums(const EmbedGradArgs &a, const EmbedGradPlan &p, cons
     const int cols = vec ? 8 * kRunThreads : 2 * kRunThreads, slabs = (a.d + cols - 1) / cols;
     const int run_blocks = p.pieces * slabs, fill_blocks = z.bits && z.begin < (size_t)a.vocab * a.d * sizeof(TG) ? 8 * 148 : 0;
     auto sum = [&](auto kernel) {
+        if (p.piece > 1024) {   // its tokens beside the rows in flight: more than the 48 KiB of a plain launch
+            const cudaError_t ea = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.piece * 8);
+            if (ea != cudaSuccess) return ea;
+        }
         return launch_k(kernel, run_blocks + fill_blocks, kRunThreads, (size_t)p.piece * 8, s, (const T *)a.dout, tok, idx,
                         a.rows, a.d, a.vocab, p.piece, slabs, run_blocks, a.scale, a.accumulate, (TG *)a.dtable, part, z);
     };

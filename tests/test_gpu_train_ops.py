@@ -182,6 +182,18 @@ def test_embed_grad_large_tables(n, d, V, dt, odt, kind):
     assert bool((base[cnt == 0] == 1).all())
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("n,d", [(1500000, 8), (2500000, 8), (4000000, 3)])
+def test_embed_grad_most_rows(dt, n, d):
+    """The longest pieces of the sorted rows, up to the most rows there may be."""
+    dout, ids = _embed_grad_case(n, d, 1000, dt, "blocks")
+    got = pkg.orthrus_embed_grad(dout, ids, 1000)
+    want, mag, cnt = _embed_grad_want(dout, ids, 1000, 1.0)
+    # a piece adds at most 4096 rows in a row, the pieces come to at most 1024
+    # partials in 8 strands: no longer chain of additions than their sum
+    within(got, want, half(dt) * want.abs() + (4096 + 1024 / 8 + 8 + 3) * U * mag)
+
+
 @pytest.mark.parametrize("n,V", [(100, 64), (9000, 64)])
 def test_embed_grad_accumulates(n, V):
     d = 48
@@ -516,13 +528,13 @@ def test_losses_full_vocabulary_rows():
     assert float(rel.max()) < 3 * half(BF)
 
 
-def test_losses_in_several_pieces():
+@pytest.mark.parametrize("dt,n,d,V", [(BF, 4000, 72, 40001), (F32, 5000, 16, 4000)])
+def test_losses_in_several_pieces(dt, n, d, V):
     """So many rows that the vocabulary is gone over in pieces, with a ragged
     last piece: every element."""
-    n, d, V = 4000, 72, 20001
-    test_ce_lm_head(BF, n, d, V)
-    test_ce_lm_head_grad(BF, n, d, V)
-    test_kl_lm_head_grad(BF, n, d, V)
+    test_ce_lm_head(dt, n, d, V)
+    test_ce_lm_head_grad(dt, n, d, V)
+    test_kl_lm_head_grad(dt, n, d, V)
 
 
 def test_offsets_past_32_bits():
