@@ -263,7 +263,7 @@ def orthrus_embed_rows(table, ids, scale=1.0, out_dtype=None, err=None):
     out_dtype = _torch.float32 if out_dtype is None else out_dtype
     od = _dtype_id("out_dtype", out_dtype)
     with _OnDevice(dev) as stream:
-        out = _torch.empty((n, d), dtype=out_dtype, device=dev)
+        out = _torch.empty(n, d, dtype=out_dtype, device=dev)
         _check("orthrus_embed_rows", lib().orthrus_embed_rows(
             table.data_ptr(), _dtype_id("table", table.dtype), V, d, ids.data_ptr(), n, float(scale), out.data_ptr(),
             od, _err_ptr(err, dev), stream))
@@ -287,7 +287,7 @@ def orthrus_embed_grad(dout, ids, vocab, scale=1.0, dtype=None, out=None, accumu
         _need_rows("out", out, fl if dtype is None else (dtype,), (vocab, d), dev)
     with _OnDevice(dev) as stream:
         if out is None:
-            out = _torch.empty((vocab, d), dtype=dout.dtype if dtype is None else dtype, device=dev)
+            out = _torch.empty(vocab, d, dtype=dout.dtype if dtype is None else dtype, device=dev)
         od = _dtype_id("dtype", out.dtype)
         ws, wp, wn = _train_ws("orthrus_embed_grad_workspace", dev, n, d, vocab)
         _check("orthrus_embed_grad", lib().orthrus_embed_grad(
@@ -302,7 +302,7 @@ def orthrus_rmsnorm(x, gain, eps):
     n, d = _need_rows("x", x, _dtypes(), (None, None))
     _need_rows("gain", gain, _dtypes(), (d,), x.device)
     with _OnDevice(x.device) as stream:
-        y = _torch.empty((n, d), dtype=gain.dtype, device=x.device)
+        y = _torch.empty(n, d, dtype=gain.dtype, device=x.device)
         _check("orthrus_rmsnorm", lib().orthrus_rmsnorm(
             x.data_ptr(), _dtype_id("x", x.dtype), gain.data_ptr(), _dtype_id("gain", gain.dtype), n, d, float(eps),
             y.data_ptr(), stream))
