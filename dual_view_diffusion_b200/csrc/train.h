@@ -33,17 +33,17 @@ struct EmbedRowsArgs {
 };
 cudaError_t launch_embed_rows(const EmbedRowsArgs &a, cudaStream_t s);
 
-// most rows sorted by one block (8192 rows: 37 us; the radix sort's six launches
-// take 45 us at 16384 rows, and no less at fewer)
-constexpr int kSortSmall = 8192;
+// most rows sorted by counting (16384 rows: 44 us; the radix sort's six launches
+// take 45, and no less at fewer)
+constexpr int kRankMost = 16384;
 constexpr int kSortTile = 2048;    // keys per block of the radix sort
 constexpr int kSortDigit = 9;      // widest radix digit
 
 struct EmbedGradPlan {
-    size_t total, o_tok[2], o_idx[2], o_hist, o_part, o_bits;
+    size_t total, o_tok[2], o_idx[2], o_hist, o_part;
     int piece;     // sorted rows per piece
     int pieces;
-    int digits, digit_bits, tiles;   // radix sort (rows > kSortSmall)
+    int digits, digit_bits, tiles;   // radix sort (rows > kRankMost)
 };
 EmbedGradPlan plan_embed_grad(int rows, int vocab, int d);
 struct EmbedGradArgs {

@@ -212,6 +212,8 @@ cudaError_t launch_embed_rows(const EmbedRowsArgs &a, cudaStream_t s)
 // the rows, so a run has to be shared by many blocks; the fixed cut and
 // order give the same bits on every call (no floating-point atomics).
 // Ids outside [0, vocab) sort behind every token and are left out.
+constexpr int kRunThreads = 128;
+
 EmbedGradPlan plan_embed_grad(int rows, int vocab, int d)
 {
     EmbedGradPlan p{};
@@ -225,14 +227,14 @@ EmbedGradPlan plan_embed_grad(int rows, int vocab, int d)
     p.digits = (bits + kSortDigit - 1) / kSortDigit;
     p.digit_bits = (bits + p.digits - 1) / p.digits;
     p.tiles = (rows + kSortTile - 1) / kSortTile;
-    p.o_hist = w.take(rows > kSortSmall ? ((size_t)p.tiles << p.digit_bits) * 4 : 0);
-    // pieces: short enough that the rows spread over the SMs, long enough
-    // that at most ~1024 partials per column wait to be joined
-    p.piece = 32;
-    while (p.piece < 4096 && rows / p.piece > 1024) p.piece *= 2;
+    p.o_hist = w.take(rows > kRankMost ? ((size_t)p.tiles << p.digit_bits) * 4 : 0);
+    // pieces: short enough that the rows spread over the SMs, long enough that
+    // about 1024 blocks, and partials per column, are the most
+    const int slabs = (d + 8 * kRunThreads - 1) / (8 * kRunThreads);
+    p.piece = 8;
+    while (p.piece < 4096 && (long)(rows / p.piece) * slabs > 1024) p.piece *= 2;
     p.pieces = (rows + p.piece - 1) / p.piece;
     p.o_part = w.take((size_t)p.pieces * 2 * d * 4);
-    p.o_bits = w.take(((size_t)vocab + 31) / 32 * 4);
     p.total = w.total;
     return p;
 }
@@ -244,114 +246,63 @@ __device__ __forceinline__ int sort_key(const int32_t *ids, int r, int vocab, un
     return id < 0 || id >= vocab ? vocab : id;
 }
 
-// Ids that do not occur get rows of zeros.  The table's first rows are
-// written beside the sort, whoever they belong to, as many as the idle SMs
-// manage meanwhile; the rest beside the sums, by blocks that skip the rows
-// whose bit says that the token occurs (8192 rows of 4096, vocabulary 151936:
-// all zeros beside the sort, then the sums, 294 us; like this 233 us, of
-// a floor of 204 us).
-struct ZeroFill {
-    char *p;              // the table, or null (accumulating)
-    size_t begin, end;    // bytes that this launch writes; the sums' launch: from begin on
-    unsigned *bits;       // one bit per id, or null: everything is written beside the sort
-    int words;
-};
+// Up to kRankMost rows: a row's place is the number of rows before it in (token,
+// row) order, counted against all of them.  64 rows per block, one per lane, 16
+// warps for each 32 rows, every warp over its share of the keys in shared memory
+// (four per broadcast read).  The count grows with the square of the rows but is
+// spread over all SMs: 15 us at 8192 rows, where a bitonic sort by one block took 37
+// (1003 rows of 64 altogether 17.4 -> 9.4 us of kernels, 8000 rows of 100 56 -> 30).
+constexpr int kRankThreads = 1024, kRankRows = 64, kRankStrands = kRankThreads / kRankRows;
 
-constexpr int kSortThreads = 1024;
-// the one-block sort takes about 5 us for every 1024 rows, 6 TB/s meanwhile is
-// this much a row; a launch of the radix sort about 10 us
-constexpr size_t kZeroPerRow = (size_t)32 << 10, kZeroPerLaunch = (size_t)64 << 20;
-
-__device__ __forceinline__ void fill_zero(const ZeroFill &z, int first_block)
+__global__ void __launch_bounds__(kRankThreads) rank_sort_kernel(const int32_t *ids, int rows, int vocab, int blocks,
+                                                                 int32_t *tok, int32_t *idx, char *zero,
+                                                                 size_t zero_bytes, unsigned *err)
 {
-    zero_span(z.p + z.begin, z.end - z.begin, (size_t)(blockIdx.x - first_block) * blockDim.x + threadIdx.x,
-              (size_t)(gridDim.x - first_block) * blockDim.x);
-}
-
-// Bitonic network over kSortThreads * E keys, thread t holding keys t E ..
-// t E + E - 1: exchanges within a thread stay in registers, within a warp go
-// through shuffles, the others through shared memory.
-template <class K, int E> constexpr int kSortHold = E * sizeof(K) > 32 ? 32 / sizeof(K) : E;   // keys of a thread in smem
-
-template <class K, int E> __device__ __forceinline__ void bitonic_sort(K (&key)[E], int n, K *sm)
-{
-    const int t = threadIdx.x;
-    for (int k = 2; k <= n; k <<= 1) {
-        for (int j = k >> 1; j >= E; j >>= 1) {
-            const int tj = j / E;
-            K other[E];
-            if (tj >= 32) {
-                constexpr int H = kSortHold<K, E>;
-#pragma unroll
-                for (int h = 0; h < E; h += H) {
-                    __syncthreads();
-#pragma unroll
-                    for (int e = 0; e < H; ++e) sm[e * kSortThreads + t] = key[h + e];
-                    __syncthreads();
-#pragma unroll
-                    for (int e = 0; e < H; ++e) other[h + e] = sm[e * kSortThreads + (t ^ tj)];
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) other[e] = __shfl_xor_sync(0xffffffffu, key[e], tj);
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const bool up = ((t * E + e) & k) == 0, low = (t & tj) == 0;
-                if ((key[e] > other[e]) == (up == low)) key[e] = other[e];
-            }
-        }
-#pragma unroll
-        for (int j = E / 2; j > 0; j >>= 1)
-            if (j < k)
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    if (e & j) continue;
-                    const bool up = ((t * E + e) & k) == 0;
-                    const K a = key[e], b = key[e + j];
-                    if ((a > b) == up) { key[e] = b; key[e + j] = a; }
-                }
-    }
-}
-
-// Up to kSortSmall rows: block 0 sorts (token, row) pairs, the other blocks
-// write the first zeros meanwhile.
-template <class K, int E>
-__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const int32_t *ids, int rows, int vocab, int row_bits,
-                                                                  int32_t *tok, int32_t *idx, ZeroFill z, unsigned *err)
-{
-    __shared__ K sm[kSortThreads * kSortHold<K, E>];
-    __shared__ int32_t last[kSortThreads];
+    extern __shared__ __align__(16) int32_t rank_keys[];
+    __shared__ int part[kRankStrands][kRankRows];
     pdl_trigger();
     pdl_wait();
-    if (blockIdx.x > 0) {
-        fill_zero(z, 1);
+    if ((int)blockIdx.x >= blocks) {   // the table's first zeros, for which the memory has time
+        zero_span(zero, zero_bytes, (size_t)(blockIdx.x - blocks) * kRankThreads + threadIdx.x,
+                  (size_t)(gridDim.x - blocks) * kRankThreads);
         return;
     }
-    if (z.bits)
-        for (int i = threadIdx.x; i < z.words; i += kSortThreads) z.bits[i] = 0;
-    int n = 2;
-    while (n < rows) n <<= 1;
-    K key[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = threadIdx.x * E + e;
-        key[e] = i < rows ? (((K)sort_key(ids, i, vocab, err) << row_bits) | (K)i) : ~(K)0;
-    }
-    bitonic_sort<K, E>(key, n, sm);
-    last[threadIdx.x] = (int32_t)(key[E - 1] >> row_bits);
+    const int n4 = (rows + 3) / 4;
+    for (int i = threadIdx.x; i < 4 * n4; i += kRankThreads) rank_keys[i] = i < rows ? sort_key(ids, i, vocab, err) : INT_MAX;
     __syncthreads();
-    int prev = threadIdx.x ? last[threadIdx.x - 1] : -1;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const int i = threadIdx.x * E + e;
-        if (i >= rows) break;
-        const int t = (int32_t)(key[e] >> row_bits);
-        tok[i] = t;
-        idx[i] = (int32_t)(key[e] & (((K)1 << row_bits) - 1));
-        if (z.bits && t != prev && t < vocab) atomicOr(&z.bits[t >> 5], 1u << (t & 31));
-        prev = t;
+    const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) & 1, strand = threadIdx.x >> 6;
+    const int first = blockIdx.x * kRankRows + 32 * group, row = first + lane;
+    const int key = row < rows ? rank_keys[row] : 0;
+    const int per = (n4 + kRankStrands - 1) / kRankStrands, c0 = min(n4, strand * per), c1 = min(n4, c0 + per);
+    const int below = min(c1, max(c0, first / 4)), mixed = min(c1, max(c0, first / 4 + 8));
+    const int4 *k4 = (const int4 *)rank_keys;
+    int count = 0;
+    // keys of rows before all of the warp's rows come first when equal, of rows after them when smaller
+#pragma unroll 8
+    for (int c = c0; c < below; ++c) {
+        const int4 k = k4[c];
+        count += (k.x <= key) + (k.y <= key) + (k.z <= key) + (k.w <= key);
     }
+    for (int c = below; c < mixed; ++c) {
+        const int4 k = k4[c];
+        const int j = 4 * c;
+        count += (k.x < key + (j < row)) + (k.y < key + (j + 1 < row)) + (k.z < key + (j + 2 < row)) +
+                 (k.w < key + (j + 3 < row));
+    }
+#pragma unroll 8
+    for (int c = mixed; c < c1; ++c) {
+        const int4 k = k4[c];
+        count += (k.x < key) + (k.y < key) + (k.z < key) + (k.w < key);
+    }
+    part[strand][32 * group + lane] = count;
+    __syncthreads();
+    const int r = blockIdx.x * kRankRows + threadIdx.x;
+    if (threadIdx.x >= kRankRows || r >= rows) return;
+    int at = 0;
+#pragma unroll
+    for (int q = 0; q < kRankStrands; ++q) at += part[q][threadIdx.x];
+    tok[at] = rank_keys[r];
+    idx[at] = r;
 }
 
 // More rows: least-significant-digit radix sort, one launch each for a
@@ -361,20 +312,11 @@ constexpr int kRadixThreads = 256, kRadixWarps = kRadixThreads / 32, kRadixPer =
 
 template <bool FIRST>
 __global__ void __launch_bounds__(kRadixThreads) radix_hist_kernel(const int32_t *src, int rows, int vocab, int tiles,
-                                                                   int shift, int bits, int *hist, ZeroFill z,
-                                                                   unsigned *err)
+                                                                   int shift, int bits, int *hist, unsigned *err)
 {
     __shared__ int h[1 << kSortDigit];
     pdl_trigger();
     pdl_wait();
-    if ((int)blockIdx.x >= tiles) {
-        if (FIRST && z.bits)
-            for (int i = (blockIdx.x - tiles) * kRadixThreads + threadIdx.x; i < z.words;
-                 i += (gridDim.x - tiles) * kRadixThreads)
-                z.bits[i] = 0;
-        fill_zero(z, tiles);
-        return;
-    }
     for (int i = threadIdx.x; i < (1 << bits); i += kRadixThreads) h[i] = 0;
     __syncthreads();
     const int base = blockIdx.x * kSortTile;
@@ -440,16 +382,11 @@ __global__ void __launch_bounds__(1024) radix_scan_kernel(int *h, int n)
 template <bool FIRST>
 __global__ void __launch_bounds__(kRadixThreads) radix_scatter_kernel(const int32_t *src_tok, const int32_t *src_idx,
                                                                       int rows, int vocab, int tiles, int shift, int bits,
-                                                                      const int *hist, int32_t *tok, int32_t *idx,
-                                                                      ZeroFill z)
+                                                                      const int *hist, int32_t *tok, int32_t *idx)
 {
     __shared__ int cnt[kRadixWarps][1 << kSortDigit];
     pdl_trigger();
     pdl_wait();
-    if ((int)blockIdx.x >= tiles) {
-        fill_zero(z, tiles);
-        return;
-    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nb = 1 << bits;
     for (int i = threadIdx.x; i < kRadixWarps * nb; i += kRadixThreads) cnt[i / nb][i % nb] = 0;
     __syncthreads();
@@ -485,11 +422,6 @@ __global__ void __launch_bounds__(kRadixThreads) radix_scatter_kernel(const int3
     for (int j = 0; j < kRadixPer; ++j) {
         const int i = base + j * 32 + lane;
         if (i >= rows) continue;
-        if (FIRST && z.bits && key[j] < vocab) {
-            unsigned *w = &z.bits[key[j] >> 5];
-            const unsigned b = 1u << (key[j] & 31);
-            if (!(*(volatile unsigned *)w & b)) atomicOr(w, b);   // (few atomics where most rows share a token)
-        }
         const int pos = cnt[warp][(key[j] >> shift) & (nb - 1)] + rank[j];
         tok[pos] = key[j];
         idx[pos] = FIRST ? i : src_idx[i];
@@ -497,14 +429,14 @@ __global__ void __launch_bounds__(kRadixThreads) radix_scatter_kernel(const int3
 }
 
 // One block per (piece, column slab): runs of equal tokens summed in fp32.
-// Blocks from run_blocks on write the remaining zeros, a warp per absent row.
-constexpr int kRunThreads = 128;
-
+// Blocks from run_blocks on write the rows of zeros of the ids from zero_from on
+// that do not occur: a warp takes `unit` table rows, its lanes look them up in
+// the sorted tokens, and the absent ones are written.
 template <class T, class TG, int VEC>
 __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const T *dout, const int32_t *tok, const int32_t *idx,
                                                               int rows, int d, int vocab, int P, int slabs,
-                                                              int run_blocks, float scale, int accumulate, TG *dtable,
-                                                              float *part, ZeroFill z)
+                                                              int run_blocks, int zero_from, int unit, float scale, int accumulate,
+                                                              TG *dtable, float *part)
 {
     constexpr int J = VEC == 8 ? 1 : 2;                       // column chunks of a thread
     constexpr int U = VEC == 8 && sizeof(T) == 4 ? 8 : 16;    // rows in flight
@@ -517,10 +449,26 @@ __global__ void __launch_bounds__(kRunThreads) run_sum_kernel(const T *dout, con
     pdl_wait();
     if ((int)blockIdx.x >= run_blocks) {
         const size_t row_bytes = (size_t)d * sizeof(TG);
-        const int warps = (gridDim.x - run_blocks) * (kRunThreads / 32);
-        for (int v = (int)(z.begin / row_bytes) + (blockIdx.x - run_blocks) * (kRunThreads / 32) + (threadIdx.x >> 5);
-             v < vocab; v += warps)
-            if (!(z.bits[v >> 5] >> (v & 31) & 1)) zero_span(z.p + (size_t)v * row_bytes, row_bytes, threadIdx.x & 31, 32);
+        const int lane = threadIdx.x & 31, step = (gridDim.x - run_blocks) * (kRunThreads / 32) * unit;
+        for (int v0 = zero_from + ((blockIdx.x - run_blocks) * (kRunThreads / 32) + (threadIdx.x >> 5)) * unit; v0 < vocab;
+             v0 += step) {
+            const int v = v0 + lane;
+            bool absent = lane < unit && v < vocab;
+            if (absent) {
+                int lo = 0, hi = rows;   // first place of a token >= v
+                while (lo < hi) {
+                    const int m = (lo + hi) >> 1;
+                    if (tok[m] < v) lo = m + 1;
+                    else hi = m;
+                }
+                absent = lo == rows || tok[lo] != v;
+            }
+            for (unsigned m = __ballot_sync(0xffffffffu, absent); m;) {   // spans of absent rows
+                const int b = __ffs(m) - 1, n = __ffs(~(m >> b)) ? __ffs(~(m >> b)) - 1 : 32;
+                zero_span((char *)dtable + (size_t)(v0 + b) * row_bytes, n * row_bytes, lane, 32);
+                m = b + n < 32 ? m >> (b + n) << (b + n) : 0;
+            }
+        }
         return;
     }
     const int piece = blockIdx.x / slabs;
@@ -665,125 +613,108 @@ __global__ void __launch_bounds__(kJoinThreads) run_join_kernel(const int32_t *t
     }
 }
 
-__global__ void __launch_bounds__(kSortThreads) fill_zero_kernel(ZeroFill z)
+__global__ void __launch_bounds__(1024) fill_zero_kernel(char *p, size_t bytes)
 {
     pdl_trigger();
     pdl_wait();
-    fill_zero(z, 0);
+    zero_span(p, bytes, (size_t)blockIdx.x * 1024 + threadIdx.x, (size_t)gridDim.x * 1024);
 }
 
 template <class T, class TG>
 static cudaError_t run_sums(const EmbedGradArgs &a, const EmbedGradPlan &p, const int32_t *tok, const int32_t *idx,
-                            const ZeroFill &z, cudaStream_t s)
+                            int zero_from, cudaStream_t s)
 {
     float *part = (float *)(a.ws + p.o_part);
     const bool vec = rows_aligned(a.dout, a.d) && rows_aligned(a.dtable, a.d);
     const int cols = vec ? 8 * kRunThreads : 2 * kRunThreads, slabs = (a.d + cols - 1) / cols;
-    const int run_blocks = p.pieces * slabs, fill_blocks = z.bits && z.begin < (size_t)a.vocab * a.d * sizeof(TG) ? 8 * 148 : 0;
+    const int run_blocks = p.pieces * slabs;
+    // zeros: about 32 KiB of table rows per warp, so that the blocks, started in
+    // order, write the table in order (8 blocks per SM that stride over it: 250 us
+    // instead of 216 for 8192 rows of 4096, vocabulary 151936, of a floor of 204)
+    const size_t row_bytes = (size_t)a.d * sizeof(TG);
+    const int unit = (int)std::max<size_t>(1, std::min<size_t>(32, 32768 / row_bytes));
+    const int units = (a.vocab - zero_from + unit - 1) / unit, per = kRunThreads / 32;
+    const int fill_blocks = (units + per - 1) / per;
     auto sum = [&](auto kernel) {
         if (p.piece > 1024) {   // its tokens beside the rows in flight: more than the 48 KiB of a plain launch
             const cudaError_t ea = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.piece * 8);
             if (ea != cudaSuccess) return ea;
         }
         return launch_k(kernel, run_blocks + fill_blocks, kRunThreads, (size_t)p.piece * 8, s, (const T *)a.dout, tok, idx,
-                        a.rows, a.d, a.vocab, p.piece, slabs, run_blocks, a.scale, a.accumulate, (TG *)a.dtable, part, z);
+                        a.rows, a.d, a.vocab, p.piece, slabs, run_blocks, zero_from, unit, a.scale, a.accumulate, (TG *)a.dtable, part);
     };
     cudaError_t e = vec ? sum(run_sum_kernel<T, TG, 8>) : sum(run_sum_kernel<T, TG, 1>);
     if (e != cudaSuccess || p.pieces < 2) return e;
     auto join = [&](auto kernel, int per) {
-        return launch_k(kernel, dim3(std::min(kJoinBlocks, p.pieces - 1), (a.d + per - 1) / per), kJoinThreads, 0, s, tok,
+        // (few columns: more blocks, each with fewer pieces to look at)
+        const int cols = (a.d + per - 1) / per, wide = std::max(kJoinBlocks, 16 * 148 / cols);
+        return launch_k(kernel, dim3(std::min(wide, p.pieces - 1), cols), kJoinThreads, 0, s, tok,
                         a.rows, a.d, a.vocab, p.pieces, p.piece, a.scale, a.accumulate, (TG *)a.dtable, (const float *)part);
     };
     return a.d % 4 == 0 ? join(run_join_kernel<TG, 4>, kJoinLanes * 4) : join(run_join_kernel<TG, 1>, kJoinLanes);
 }
 
-template <class K>
-static cudaError_t sort_small(const EmbedGradArgs &a, int row_bits, int32_t *tok, int32_t *idx, const ZeroFill &z, int fill,
-                              cudaStream_t s)
-{
-    auto go = [&](auto kernel) {
-        return launch_k(kernel, 1 + fill, kSortThreads, 0, s, a.ids, a.rows, a.vocab, row_bits, tok, idx, z, a.err);
-    };
-    // keys per thread: as few as hold the rows
-    return a.rows <= kSortThreads ? go(sort_small_kernel<K, 1>)
-           : a.rows <= 2 * kSortThreads ? go(sort_small_kernel<K, 2>)
-           : a.rows <= 4 * kSortThreads ? go(sort_small_kernel<K, 4>)
-                                        : go(sort_small_kernel<K, 8>);
-}
-
 cudaError_t launch_embed_grad(const EmbedGradArgs &a, cudaStream_t s)
 {
-    const size_t row_bytes = (size_t)a.d * (a.dtable_dtype == ORTHRUS_BF16 ? 2 : 4), bytes = (size_t)a.vocab * row_bytes;
-    ZeroFill z{};
-    if (!a.accumulate) z.p = (char *)a.dtable;
-    // the next `most` bytes of zeros (whole rows) go to the next launch; its
-    // blocks for them: two of 1024 threads per SM, fewer for few bytes
-    auto share = [&](size_t most) {
-        z.begin = z.end;
-        if (!z.p) return 0;
-        z.end = bytes - z.begin <= most ? bytes : z.begin + most / row_bytes * row_bytes;
-        return (int)std::min<size_t>(2 * 148, (z.end - z.begin + 16383) / 16384);
-    };
     cudaError_t e;
     if (a.rows == 0) {
-        const int fill = share(bytes);
-        return fill ? launch_k(fill_zero_kernel, fill, kSortThreads, 0, s, z) : cudaSuccess;
+        if (a.accumulate) return cudaSuccess;
+        const size_t bytes = (size_t)a.vocab * a.d * (a.dtable_dtype == ORTHRUS_BF16 ? 2 : 4);
+        return launch_k(fill_zero_kernel, (int)std::min<size_t>(2 * 148, (bytes + 16383) / 16384), 1024, 0, s,
+                        (char *)a.dtable, bytes);
     }
     const EmbedGradPlan p = plan_embed_grad(a.rows, a.vocab, a.d);
-    const size_t beside = a.rows <= kSortSmall ? std::max(a.rows, 1024) * kZeroPerRow
-                                               : 2 * p.digits * (kZeroPerLaunch / row_bytes * row_bytes);
-    if (z.p && bytes > beside) {
-        z.bits = (unsigned *)(a.ws + p.o_bits);
-        z.words = (a.vocab + 31) / 32;
-    }
     int32_t *tok[2] = {(int32_t *)(a.ws + p.o_tok[0]), (int32_t *)(a.ws + p.o_tok[1])};
     int32_t *idx[2] = {(int32_t *)(a.ws + p.o_idx[0]), (int32_t *)(a.ws + p.o_idx[1])};
-    int cur = 0;
-    if (a.rows <= kSortSmall) {
-        int n = 2, row_bits = 1;
-        while (n < a.rows) { n <<= 1; ++row_bits; }
-        int key_bits = 1;
-        while (key_bits < 31 && (a.vocab >> key_bits) != 0) ++key_bits;
-        const int fill = share(beside);
-        // 32-bit keys while (token, row) fits below the padding key
-        e = key_bits + row_bits <= 31 ? sort_small<uint32_t>(a, row_bits, tok[0], idx[0], z, fill, s)
-                                      : sort_small<uint64_t>(a, row_bits, tok[0], idx[0], z, fill, s);
+    int cur = 0, zero_from = a.accumulate ? a.vocab : 0;   // the sums' launch writes the zeros from this id on
+    if (a.rows <= kRankMost) {
+        const size_t smem = (size_t)(a.rows + 3) / 4 * 16;
+        if (smem > 40960) {   // (beside the partial counts, within 48 KiB of a plain launch)
+            e = cudaFuncSetAttribute(rank_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRankMost * 4);
+            if (e != cudaSuccess) return e;
+        }
+        // beside the sort (4 us, and 15 us at 8192 rows) the memory writes 6 TB/s of zeros
+        const int blocks = (a.rows + kRankRows - 1) / kRankRows;
+        const size_t row_bytes = (size_t)a.d * (a.dtable_dtype == ORTHRUS_BF16 ? 2 : 4);
+        if (!a.accumulate)
+            zero_from = (int)std::min<size_t>(a.vocab, (((size_t)16 << 20) + (size_t)a.rows * a.rows) / row_bytes);
+        const size_t zero_bytes = a.accumulate ? 0 : zero_from * row_bytes;
+        const int fill = (int)std::min<size_t>(148, (zero_bytes + 32767) / 32768);
+        e = launch_k(rank_sort_kernel, blocks + fill, kRankThreads, smem, s, a.ids, a.rows, a.vocab, blocks, tok[0], idx[0],
+                     (char *)a.dtable, zero_bytes, a.err);
         if (e != cudaSuccess) return e;
     } else {
         int *hist = (int *)(a.ws + p.o_hist);
         const int32_t *st = a.ids, *si = nullptr;
         for (int pass = 0; pass < p.digits; ++pass) {
             const int shift = pass * p.digit_bits;
-            int fill = 4 * share(kZeroPerLaunch);   // (these blocks are a quarter as large)
             if (pass == 0)
-                e = launch_k(radix_hist_kernel<true>, p.tiles + fill, kRadixThreads, 0, s, st, a.rows, a.vocab, p.tiles,
-                             shift, p.digit_bits, hist, z, a.err);
+                e = launch_k(radix_hist_kernel<true>, p.tiles, kRadixThreads, 0, s, st, a.rows, a.vocab, p.tiles, shift,
+                             p.digit_bits, hist, a.err);
             else
-                e = launch_k(radix_hist_kernel<false>, p.tiles + fill, kRadixThreads, 0, s, st, a.rows, a.vocab, p.tiles,
-                             shift, p.digit_bits, hist, z, a.err);
+                e = launch_k(radix_hist_kernel<false>, p.tiles, kRadixThreads, 0, s, st, a.rows, a.vocab, p.tiles, shift,
+                             p.digit_bits, hist, a.err);
             if (e != cudaSuccess) return e;
             e = launch_k(radix_scan_kernel, 1, 1024, 0, s, hist, p.tiles << p.digit_bits);
             if (e != cudaSuccess) return e;
-            fill = 4 * share(kZeroPerLaunch);
             if (pass == 0)
-                e = launch_k(radix_scatter_kernel<true>, p.tiles + fill, kRadixThreads, 0, s, st, si, a.rows, a.vocab,
-                             p.tiles, shift, p.digit_bits, (const int *)hist, tok[0], idx[0], z);
+                e = launch_k(radix_scatter_kernel<true>, p.tiles, kRadixThreads, 0, s, st, si, a.rows, a.vocab, p.tiles,
+                             shift, p.digit_bits, (const int *)hist, tok[0], idx[0]);
             else
-                e = launch_k(radix_scatter_kernel<false>, p.tiles + fill, kRadixThreads, 0, s, st, si, a.rows, a.vocab,
-                             p.tiles, shift, p.digit_bits, (const int *)hist, tok[pass & 1], idx[pass & 1], z);
+                e = launch_k(radix_scatter_kernel<false>, p.tiles, kRadixThreads, 0, s, st, si, a.rows, a.vocab, p.tiles,
+                             shift, p.digit_bits, (const int *)hist, tok[pass & 1], idx[pass & 1]);
             if (e != cudaSuccess) return e;
             cur = pass & 1;
             st = tok[cur];
             si = idx[cur];
         }
     }
-    z.begin = z.end;
     const bool ib = a.dout_dtype == ORTHRUS_BF16, ob = a.dtable_dtype == ORTHRUS_BF16;
     if (ib)
-        return ob ? run_sums<bf16, bf16>(a, p, tok[cur], idx[cur], z, s)
-                  : run_sums<bf16, float>(a, p, tok[cur], idx[cur], z, s);
-    return ob ? run_sums<float, bf16>(a, p, tok[cur], idx[cur], z, s)
-              : run_sums<float, float>(a, p, tok[cur], idx[cur], z, s);
+        return ob ? run_sums<bf16, bf16>(a, p, tok[cur], idx[cur], zero_from, s)
+                  : run_sums<bf16, float>(a, p, tok[cur], idx[cur], zero_from, s);
+    return ob ? run_sums<float, bf16>(a, p, tok[cur], idx[cur], zero_from, s)
+              : run_sums<float, float>(a, p, tok[cur], idx[cur], zero_from, s);
 }
 
 // ---------------------------------------------------------------- RMSNorm

@@ -141,7 +141,7 @@ def test_embed_grad(dt, odt, n, d, V, kind):
 
 
 def test_embed_grad_huge_vocabulary_keys():
-    """Token ids that need 64-bit (token, row) keys in the one-block sort."""
+    """Token ids up to the largest vocabulary."""
     n, d, V = 5000, 1, 3999999
     dout, ids = _embed_grad_case(n, d, V, F32, "any")
     ids[:100] = V - 1
@@ -150,10 +150,11 @@ def test_embed_grad_huge_vocabulary_keys():
     within(got, want, half(F32) * want.abs() + (cnt[:, None] + 3) * U * mag)
 
 
-@pytest.mark.parametrize("n", [1023, 1025, 2048, 3000, 4096, 5000])
+@pytest.mark.parametrize("n", [63, 65, 1023, 1025, 2048, 3000, 4096, 5000, 11000, 16383, 16384, 16385])
 @pytest.mark.parametrize("V", [50, 3999999])
-def test_embed_grad_one_block_sort(n, V):
-    """Every number of keys per thread, 32- and 64-bit keys."""
+def test_embed_grad_sorts(n, V):
+    """Rows around the edges of the counting sort's blocks and its end, where the
+    radix sort takes over."""
     d = 3
     dout, ids = _embed_grad_case(n, d, V, F32, "padded")
     got = pkg.orthrus_embed_grad(dout, ids, V)
@@ -163,7 +164,8 @@ def test_embed_grad_one_block_sort(n, V):
 
 @pytest.mark.parametrize("n,d,V,dt,odt,kind", [
     (300, 1000, 40000, BF, BF, "any"), (9000, 129, 151936, BF, F32, "blocks"), (2500, 33, 1100000, F32, BF, "padded"),
-    (5, 4096, 9000, BF, BF, "one"), (9000, 1000, 134217, BF, BF, "any"), (9000, 1500, 151936, BF, BF, "blocks"), (70000, 8, 2200000, BF, F32, "any"), (3, 65536, 600, F32, BF, "any")])
+    (5, 4096, 9000, BF, BF, "one"), (9000, 1000, 134217, BF, BF, "any"), (9000, 1500, 151936, BF, BF, "blocks"), (20000, 129, 151936, BF, F32, "blocks"),
+    (70000, 8, 2200000, BF, F32, "any"), (3, 65536, 600, F32, BF, "any")])
 def test_embed_grad_large_tables(n, d, V, dt, odt, kind):
     """Tables whose zeros are written beside the sums, whatever they held."""
     dout, ids = _embed_grad_case(n, d, V, dt, kind)
@@ -194,7 +196,7 @@ def test_embed_grad_most_rows(dt, n, d):
     within(got, want, half(dt) * want.abs() + (4096 + 1024 / 8 + 8 + 3) * U * mag)
 
 
-@pytest.mark.parametrize("n,V", [(100, 64), (9000, 64)])
+@pytest.mark.parametrize("n,V", [(100, 64), (9000, 64), (17000, 64)])
 def test_embed_grad_accumulates(n, V):
     d = 48
     dout, ids = _embed_grad_case(n, d, V, BF, "padded")
