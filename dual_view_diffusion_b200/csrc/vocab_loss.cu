@@ -29,6 +29,7 @@ constexpr int kStK = 32;           // k per step
 constexpr int kStThreads = 256;
 constexpr int kStFlush = 4;        // steps per partial sum (128 products)
 constexpr int kStLoads = kSt * kStK / kStThreads;
+constexpr int kStBufs = 4;         // steps in shared memory
 
 // A strided operand: element (row, k).  With `live`, a k whose byte is zero
 // reads as zeros whatever it holds.
@@ -59,6 +60,7 @@ template <class T, bool K> struct StLoader {
     const T *p;          // first element of the next step
     size_t stride, step, k, kmax;
     int r, kk, left;     // left: rows from r on
+    unsigned char alive[K ? 1 : kStLoads];   // of the next step's k, read a step ahead
     __device__ __forceinline__ StLoader(const Operand<T> &o, int row0, size_t k0, size_t k1) : op(o), kmax(k1)
     {
         const int l = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -69,24 +71,32 @@ template <class T, bool K> struct StLoader {
         p = o.p + (size_t)(row0 + r) * o.row_stride + k * o.k_stride;
         stride = K ? 8 * o.row_stride : 4 * o.k_stride;
         step = kStK * o.k_stride;
+        peek();
+    }
+    __device__ __forceinline__ void peek()
+    {
+        if constexpr (!K) {
+#pragma unroll
+            for (int q = 0; q < kStLoads; ++q) alive[q] = op.live && k + 4 * q < kmax ? op.live[k + 4 * q] : 1;
+        }
     }
     __device__ __forceinline__ void load(float (&s)[kStK][kSt + 4])
     {
 #pragma unroll
         for (int q = 0; q < kStLoads; ++q) {
-            const bool ok = K ? 8 * q < left && k < kmax
-                              : left > 0 && k + 4 * q < kmax && !(op.live && !op.live[k + 4 * q]);
+            const bool ok = K ? 8 * q < left && k < kmax : left > 0 && k + 4 * q < kmax && alive[K ? 0 : q];
             st_put(K ? &s[kk][r + 8 * q] : &s[kk + 4 * q][r], p + q * stride, op.p, ok);
         }
         p += step;
         k += kStK;
+        peek();
     }
 };
 static_assert(kStThreads == 8 * 32 && kSt == 64 && kStK == 32, "StLoader's cut of a step");
 
 union StSmem {
     struct {
-        float a[2][kStK][kSt + 4], b[2][kStK][kSt + 4];   // two steps: one is loaded under the other's products
+        float a[kStBufs][kStK][kSt + 4], b[kStBufs][kStK][kSt + 4];   // a step's products run under the next ones' loads
     };
     float z[kSt][kSt + 1];
 };
@@ -106,14 +116,18 @@ __device__ void simt_tile(const Operand<TA> &A, const Operand<TB> &B, int m0, in
         for (int j = 0; j < 4; ++j) { acc[i][j] = 0.f; part[i][j] = 0.f; }
     StLoader<TA, AK> la(A, m0, k0, k1);
     StLoader<TB, BK> lb(B, n0, k0, k1);
-    if (k0 < k1) { la.load(sm.a[0]); lb.load(sm.b[0]); }
-    asm volatile("cp.async.commit_group;\n" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < kStBufs - 1; ++i) {
+        if (k0 + i * kStK < k1) { la.load(sm.a[i]); lb.load(sm.b[i]); }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    }
     int step = 0;
     for (size_t k = k0; k < k1; k += kStK) {
-        const int buf = step & 1;
-        if (k + kStK < k1) { la.load(sm.a[buf ^ 1]); lb.load(sm.b[buf ^ 1]); }
-        asm volatile("cp.async.commit_group;\ncp.async.wait_group 1;\n" ::: "memory");
-        __syncthreads();
+        const int buf = step % kStBufs, next = (step + kStBufs - 1) % kStBufs;
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(kStBufs - 2) : "memory");
+        __syncthreads();   // (the buffer loaded next was read in the step before)
+        if (k + (kStBufs - 1) * kStK < k1) { la.load(sm.a[next]); lb.load(sm.b[next]); }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
 #pragma unroll
         for (int kk = 0; kk < kStK; ++kk) {
             const float4 a = *(const float4 *)&sm.a[buf][kk][ty * 4], b = *(const float4 *)&sm.b[buf][kk][tx * 4];
@@ -123,7 +137,6 @@ __device__ void simt_tile(const Operand<TA> &A, const Operand<TB> &B, int m0, in
 #pragma unroll
                 for (int j = 0; j < 4; ++j) part[i][j] = fmaf(av[i], bv[j], part[i][j]);
         }
-        __syncthreads();
         if (++step % kStFlush == 0 || k + kStK >= k1)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -131,6 +144,7 @@ __device__ void simt_tile(const Operand<TA> &A, const Operand<TB> &B, int m0, in
                 for (int j = 0; j < 4; ++j) { acc[i][j] += part[i][j]; part[i][j] = 0.f; }
     }
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    __syncthreads();
 }
 
 // The shift of a sum of exponentials whose maximum is m: 0 where every term is
@@ -143,7 +157,8 @@ template <class T>
 __global__ void __launch_bounds__(kStThreads) ce_tile_simt(const T *h, const T *w, const int32_t *targets, int N, int d,
                                                            int V, float2 *rec, float *zt)
 {
-    __shared__ __align__(16) StSmem sm;
+    extern __shared__ __align__(16) unsigned char st_smem[];
+    StSmem &sm = *(StSmem *)st_smem;
     pdl_wait();
     const int m0 = blockIdx.y * kSt, n0 = blockIdx.x * kSt;
     float acc[4][4];
@@ -271,7 +286,8 @@ cudaError_t launch_ce_finalize(const float2 *rec, const float *zt, const LossArg
 template <class T, bool KL>
 __global__ void __launch_bounds__(kStThreads) dz_tile_simt(LossArgs a, int v0, int Vp, float *dz, unsigned char *alive)
 {
-    __shared__ __align__(16) StSmem sm;
+    extern __shared__ __align__(16) unsigned char st_smem[];
+    StSmem &sm = *(StSmem *)st_smem;
     pdl_wait();
     const int m0 = blockIdx.y * kSt, n0 = v0 + blockIdx.x * kSt, d = a.d;
     const int vend = min(a.V, v0 + Vp);
@@ -355,7 +371,8 @@ template <class T>
 __global__ void __launch_bounds__(kStThreads) grads_simt(Operand<float> dz, Operand<T> w, GradGemm gh, unsigned h_blocks,
                                                          Operand<float> dzt, Operand<T> h, GradGemm gw)
 {
-    __shared__ __align__(16) StSmem sm;
+    extern __shared__ __align__(16) unsigned char st_smem[];
+    StSmem &sm = *(StSmem *)st_smem;
     pdl_wait();
     if (blockIdx.x < h_blocks) grad_tile<float, T, true, T>(dz, w, gh, blockIdx.x, sm);
     else grad_tile<float, T, false, T>(dzt, h, gw, blockIdx.x - h_blocks, sm);
@@ -430,13 +447,20 @@ size_t loss_grad_workspace(int N, int d, int V, int dtype, int want_dw, int kl)
 }
 
 // ---------------------------------------------------------------- launches
+template <class... K, class... A>
+static cudaError_t st_launch(void (*kernel)(K...), dim3 grid, cudaStream_t s, A... args)
+{
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(StSmem));
+    return e != cudaSuccess ? e : launch_k(kernel, grid, kStThreads, sizeof(StSmem), s, args...);
+}
+
 template <class T> static cudaError_t loss_fwd_simt(const LossArgs &a, cudaStream_t s)
 {
     WsPlan w;
     const int nt = (a.V + kSt - 1) / kSt;
     float2 *rec = (float2 *)(a.ws + w.take((size_t)nt * a.N * sizeof(float2)));
     float *zt = (float *)(a.ws + w.take((size_t)a.N * 4));
-    cudaError_t e = launch_k(ce_tile_simt<T>, dim3(nt, (a.N + kSt - 1) / kSt), kStThreads, 0, s, (const T *)a.h,
+    cudaError_t e = st_launch(ce_tile_simt<T>, dim3(nt, (a.N + kSt - 1) / kSt), s, (const T *)a.h,
                              (const T *)a.w, a.targets, a.N, a.d, a.V, rec, zt);
     if (e != cudaSuccess) return e;
     return launch_ce_finalize(rec, zt, a, nt, 0, s);
@@ -452,8 +476,8 @@ template <class T> static cudaError_t loss_grad_simt(const LossArgs &a, cudaStre
     for (int v0 = 0; v0 < a.V; v0 += p.piece) {
         const int nv = std::min(p.piece, a.V - v0);
         const dim3 gz((nv + kSt - 1) / kSt, mt);
-        cudaError_t e = a.kl ? launch_k(dz_tile_simt<T, true>, gz, kStThreads, 0, s, a, v0, p.piece, dz, alive)
-                             : launch_k(dz_tile_simt<T, false>, gz, kStThreads, 0, s, a, v0, p.piece, dz, alive);
+        cudaError_t e = a.kl ? st_launch(dz_tile_simt<T, true>, gz, s, a, v0, p.piece, dz, alive)
+                             : st_launch(dz_tile_simt<T, false>, gz, s, a, v0, p.piece, dz, alive);
         if (e != cudaSuccess) return e;
         const Operand<float> A{dz, (size_t)p.piece, 1, a.N, nullptr};
         const Operand<T> B{(const T *)a.w + (size_t)v0 * a.d, 1, (size_t)a.d, a.d, nullptr};
@@ -466,7 +490,7 @@ template <class T> static cudaError_t loss_grad_simt(const LossArgs &a, cudaStre
         GradGemm gw{};
         gw.M = nv; gw.N = a.d; gw.K = a.N; gw.splits = 1; gw.out = a.dw ? (T *)a.dw + (size_t)v0 * a.d : nullptr;
         const unsigned hb = dt * mt * p.splits, wb = a.dw ? dt * ((nv + kSt - 1) / kSt) : 0;
-        e = launch_k(grads_simt<T>, hb + wb, kStThreads, 0, s, A, B, g, hb, At, Bh, gw);
+        e = st_launch(grads_simt<T>, hb + wb, s, A, B, g, hb, At, Bh, gw);
         if (e != cudaSuccess) return e;
     }
     return direct ? cudaSuccess : launch_part_sum(part, p.splits, (size_t)a.N * a.d, a.dh, a.dtype, s);
