@@ -32,9 +32,9 @@
 // its TMEM.
 //
 // Measured: 4096 rows of 4096 over 151936 ids, forward 3.4 to 3.6 ms (1.4 to 1.5
-// PFLOP/s, the sustained rate of a library product), both gradients 12.1 ms
-// (three products, 1.26 PFLOP/s; tensor pipe 81 to 85 % active, the rest the
-// ramps of a launch per product and piece).  Few rows: one row of 2048, 113 us
+// PFLOP/s, the sustained rate of a library product), both gradients 11.7 to 12.1 ms
+// (three products, 1.3 PFLOP/s; tensor pipe 80 to 87 % active, the rest the
+// ramps of a launch per product and piece, and L2 waits).  Few rows: one row of 2048, 113 us
 // of 97 for W's 622 MB; the gradients read W twice (31 rows: 207 us, of 193 for
 // that).  A narrow product is close to its own bound there too: each MMA takes
 // as long as a 256-column one, which passes W at 52 GB/s per SM.
