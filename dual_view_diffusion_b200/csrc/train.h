@@ -71,6 +71,23 @@ size_t norm_grad_workspace(int rows, int d);
 cudaError_t launch_norm_grad(const NormArgs &a, cudaStream_t s);
 
 // -------------------------------------------------------- vocabulary loss
+// acc += the products of eight bf16 pairs (each exact in fp32)
+__device__ __forceinline__ void dot8(uint4 u, uint4 v, float (&acc)[4])
+{
+    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        acc[k] = fmaf(__uint_as_float(uu[k] << 16), __uint_as_float(vv[k] << 16), acc[k]);
+        acc[k] = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(vv[k] & 0xffff0000u), acc[k]);
+    }
+}
+__device__ __forceinline__ double warp_sum_f64(double v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // One loss call: z = h W^T over V ids.  KL: h holds the AR rows, h2 the
 // diffusion rows, and lse / lse2 their log-sum-exps.
 struct LossArgs {

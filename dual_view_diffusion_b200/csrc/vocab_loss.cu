@@ -214,15 +214,7 @@ __global__ void __launch_bounds__(kFinThreads) ce_finalize_kernel(const float2 *
                 const uint4 *pw = (const uint4 *)((const bf16 *)a.w + (size_t)t * a.d);
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
-                for (int i = lane; i < a.d / 8; i += 32) {
-                    const uint4 u = ph[i], v = pw[i];
-                    const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, vv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        acc[k] = fmaf(__uint_as_float(uu[k] << 16), __uint_as_float(vv[k] << 16), acc[k]);
-                        acc[k] = fmaf(__uint_as_float(uu[k] & 0xffff0000u), __uint_as_float(vv[k] & 0xffff0000u), acc[k]);
-                    }
-                }
+                for (int i = lane; i < a.d / 8; i += 32) dot8(ph[i], pw[i], acc);
                 const float z = warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
                 if (lane == 0) sz[w] = z;
             }
@@ -320,7 +312,7 @@ __global__ void __launch_bounds__(kStThreads) dz_tile_simt(LossArgs a, int v0, i
             if (v >= vend) continue;
             float x;
             if (KL) x = expf(z2[i][j] - lse2) - expf(z[i][j] - lse);
-            else x = expf(z[i][j] - lse) - (v == t ? 1.f : 0.f);
+            else x = v == t ? expm1f(z[i][j] - lse) : expf(z[i][j] - lse);   // (a likely target's 1 - p keeps its digits)
             dz[(size_t)row * Vp + (v - v0)] = g == 0.f ? 0.f : g * x;
         }
     }

@@ -9,7 +9,8 @@
 // products is the operands' order in memory and the epilogue:
 //
 //   LSE   z = h W^T          epilogue: (max, sum exp) per (row, tile), target logit
-//   DZ    z = h W^T          epilogue: dz = g (exp(z - lse) - [v = t]), bf16
+//   DZ    z = h W^T          epilogue: dz = g exp(z - lse), the target's from
+//                            vl_target_kernel, bf16
 //   DZKL  z of interleaved (AR, diffusion) rows: dz = g (p_diff - p_AR), bf16
 //   DH    dh += dz W         A = dz rows, B = W read along its rows (MN-major)
 //   DW    dW  = dz^T h       both operands MN-major
@@ -80,6 +81,7 @@ struct VlJob {
     // epilogue
     const int32_t *targets;
     const float *lse, *lse2, *g;
+    const float *et;     // DZ, DZ_T: exp(z - lse) - 1 of the rows' targets
     float2 *rec;         // LSE: [nt][M]; LSE_T: [groups of 32 ids][N]
     float *zt;           // LSE: the rows' target logits
     bf16 *dz;            // DZ_T: [rows][pitch]
@@ -242,11 +244,11 @@ struct VlSmem {
 };
 // Behind the ring: LSE, the second warps' (maximum, sum) of a tile, per
 // accumulator; the transposed kinds, per column (row of h) lse * log2 e,
-// upstream gradient and target; DZ, DZKL and DW, 4 KiB per epilogue warp.
+// upstream gradient, target and its dz; DZ, DZKL and DW, 4 KiB per epilogue warp.
 union VlTail {
     float2 half[2][128];
     struct {
-        float k[kVlNMax], g[kVlNMax];
+        float k[kVlNMax], g[kVlNMax], e[kVlNMax];
         int t[kVlNMax];
     } col;
     unsigned char store[kVlEpi / 32][4096];
@@ -332,9 +334,10 @@ __device__ __forceinline__ void vl_box_send(const CUtensorMap *map, int x, int y
 __device__ __forceinline__ void vl_epi_dz(const VlJob &jb, const VlTile &x, int row, uint32_t taddr, int half, int lane,
                                           uint32_t buf, unsigned *err)
 {
-    float g = 0.f, k = 0.f;
+    float g = 0.f, k = 0.f, et = 0.f;
     int t = -1;
     if (row < jb.M) {
+        et = jb.et[row];
         const int id = jb.targets[row];
         if (id >= jb.V && x.n0 == 0 && jb.v0 == 0 && half == 0 && err) raise_err(err, ORTHRUS_DEVERR_TOKEN);
         if (id >= 0 && id < jb.V) { g = jb.g[row]; t = id - jb.v0 - x.n0; }
@@ -350,8 +353,7 @@ __device__ __forceinline__ void vl_epi_dz(const VlJob &jb, const VlTile &x, int 
             vl_tmem_ld32(taddr + c + q, r);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                float e = vl_exp2(fmaf(r[i], kLog2e, -k));
-                if (c + q + i == t) e -= 1.f;
+                const float e = c + q + i == t ? et : vl_exp2(fmaf(r[i], kLog2e, -k));
                 // rows without a share and columns past the vocabulary are exact zeros
                 r[i] = g == 0.f || c + q + i >= nv ? 0.f : g * e;
             }
@@ -446,7 +448,7 @@ __device__ __forceinline__ void vl_columns(const VlJob &jb, VlTail &tail, unsign
 {
     const int c = threadIdx.x;
     if (c >= kVlNMax) return;
-    float k = 0.f, g = 0.f;
+    float k = 0.f, g = 0.f, e = 0.f;
     int t = -1;
     if (c < jb.N) {
         if (jb.kind == VL_DZKL_T) {
@@ -455,12 +457,14 @@ __device__ __forceinline__ void vl_columns(const VlJob &jb, VlTail &tail, unsign
         } else {
             k = jb.lse[c] * kLog2e;
             t = jb.targets[c];
+            e = jb.et[c];
             if (t >= 0 && t < jb.V) g = jb.g[c];
             if (t >= jb.V && blockIdx.x == 0 && err) raise_err(err, ORTHRUS_DEVERR_TOKEN);
         }
     }
     tail.col.k[c] = k;
     tail.col.g[c] = g;
+    tail.col.e[c] = e;
     tail.col.t[c] = t;
 }
 static_assert(kVlThreads >= kVlNMax, "one column per thread");
@@ -514,8 +518,7 @@ __device__ __forceinline__ void vl_epi_dz_t(const VlJob &jb, const VlTail &tail,
         for (int j = 0; j < 32; ++j) {
             if (c + j >= jb.N) break;
             const float g = tail.col.g[c + j];
-            float e = vl_exp2(fmaf(r[j], kLog2e, -tail.col.k[c + j]));
-            if (tail.col.t[c + j] == v) e -= 1.f;
+            const float e = tail.col.t[c + j] == v ? tail.col.e[c + j] : vl_exp2(fmaf(r[j], kLog2e, -tail.col.k[c + j]));
             jb.dz[(size_t)(c + j) * jb.pitch + i] = __float2bfloat16_rn(g == 0.f || !live ? 0.f : g * e);
         }
     }
@@ -732,18 +735,39 @@ __global__ void __launch_bounds__(256) vl_interleave_kernel(const uint4 *ra, con
     }
 }
 
-// The hidden rows with the rows that take no part zeroed, for dW = dz^T h: a
-// padding row's dz is zero, but zero times a NaN or an infinity in its
-// hidden row would not be.
-__global__ void __launch_bounds__(256) vl_clean_kernel(const uint4 *h, const int32_t *targets, const float *g, int V,
-                                                       uint4 *out, int vecs)
+// Per row of the cross entropy, what its target's dz is made of: exp(z_t - lse)
+// - 1, with z_t taken again as a dot product in fp32 parts and a double sum.  The
+// tensor cores' accumulator truncates, by up to about 1e-5 of a logit: to every
+// other id that is 1e-4 of its probability, but of a likely target's 1 - p it
+// was most (measured at 600 rows of 4096 over 20000 ids, error of a row's dh:
+// 7 % at p = 0.999 and 84 % at p = 0.9999; 0.25 % and 0.5 % so, the latter the
+// rounding of a log-sum-exp near 16 to fp32).
+// For dW = dz^T h (out), also the hidden rows with the rows that take no part
+// zeroed: a padding row's dz is zero, but zero times a NaN or an infinity in
+// its hidden row would not be.
+__global__ void __launch_bounds__(256) vl_target_kernel(const uint4 *h, const uint4 *w, const int32_t *targets,
+                                                        const float *lse, const float *g, int V, float *et, uint4 *out,
+                                                        int vecs)
 {
+    __shared__ double part[8];
     pdl_trigger();
     pdl_wait();
     const int r = blockIdx.x, t = targets[r];
     const bool live = t >= 0 && t < V && g[r] != 0.f;
-    for (int i = threadIdx.x; i < vecs; i += 256)
-        out[(size_t)r * vecs + i] = live ? h[(size_t)r * vecs + i] : make_uint4(0, 0, 0, 0);
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int i = threadIdx.x; i < vecs; i += 256) {
+        const uint4 u = live ? h[(size_t)r * vecs + i] : make_uint4(0, 0, 0, 0);
+        if (live) dot8(u, w[(size_t)t * vecs + i], acc);
+        if (out) out[(size_t)r * vecs + i] = u;
+    }
+    const double z = warp_sum_f64((double)(acc[0] + acc[1]) + (double)(acc[2] + acc[3]));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = z;
+    __syncthreads();
+    if (threadIdx.x) return;
+    double s = part[0];
+#pragma unroll
+    for (int k = 1; k < 8; ++k) s += part[k];
+    et[r] = live ? expm1f((float)(s - (double)lse[r])) : 0.f;
 }
 
 // ---------------------------------------------------------------- host
@@ -833,7 +857,7 @@ cudaError_t loss_fwd_tc(const LossArgs &a, cudaStream_t s)
 }
 
 struct VlPlan {
-    size_t total, o_dz, o_part, o_h;
+    size_t total, o_dz, o_part, o_h, o_et;
     int piece, splits, zrows;
     bool z_narrow, h_narrow;
 };
@@ -855,6 +879,7 @@ static VlPlan vl_plan(int N, int d, int V, int want_dw, int kl)
     p.o_dz = w.take((size_t)N * p.piece * 2);
     p.o_part = w.take((size_t)p.splits * N * d * 4);
     p.o_h = w.take(kl ? (size_t)2 * N * d * 2 : want_dw ? (size_t)N * d * 2 : 0);
+    p.o_et = w.take(kl ? 0 : (size_t)N * 4);
     p.total = w.total;
     return p;
 }
@@ -866,12 +891,13 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
     const int N = a.N, d = a.d;
     const VlPlan pl = vl_plan(N, d, a.V, a.dw != nullptr, a.kl);
     bf16 *dz = (bf16 *)(a.ws + pl.o_dz), *hx = (bf16 *)(a.ws + pl.o_h);
-    float *part = (float *)(a.ws + pl.o_part);
-    cudaError_t e = cudaSuccess;
+    float *part = (float *)(a.ws + pl.o_part), *et = (float *)(a.ws + pl.o_et);
+    cudaError_t e;
     if (a.kl)
         e = launch_k(vl_interleave_kernel, N, 256, 0, s, (const uint4 *)a.h, (const uint4 *)a.h2, a.g, (uint4 *)hx, d / 8);
-    else if (a.dw)
-        e = launch_k(vl_clean_kernel, N, 256, 0, s, (const uint4 *)a.h, a.targets, a.g, a.V, (uint4 *)hx, d / 8);
+    else
+        e = launch_k(vl_target_kernel, N, 256, 0, s, (const uint4 *)a.h, (const uint4 *)a.w, a.targets, a.lse_in, a.g, a.V,
+                     et, a.dw ? (uint4 *)hx : (uint4 *)nullptr, d / 8);
     if (e != cudaSuccess) return e;
     const int zbn = pl.z_narrow ? vl_narrow_bn(pl.zrows) : kVlNMax, hbn = pl.h_narrow ? vl_narrow_bn(N) : kVlNMax;
     const int wk = (int)std::min<size_t>(kVlK, up(N, 16));   // k of dW's chunks
@@ -898,7 +924,7 @@ cudaError_t loss_grad_tc(const LossArgs &a, cudaStream_t s)
             j.chunks = (d + kVlK - 1) / kVlK; j.splits = 1; j.bn = zbn;
             j.mt = (j.M + kVlM - 1) / kVlM; j.nt = (j.N + zbn - 1) / zbn;
             (pl.z_narrow ? j.a_off : j.b_off) = v0;
-            j.targets = a.targets; j.lse = a.lse_in; j.lse2 = a.lse2_in; j.g = a.g;
+            j.targets = a.targets; j.lse = a.lse_in; j.lse2 = a.lse2_in; j.g = a.g; j.et = et;
             j.dz = dz; j.v0 = v0; j.V = a.V; j.pitch = pl.piece;
             j.a = pl.z_narrow ? zw : zh; j.b = pl.z_narrow ? zh : zw; j.c = dzs;
             p.err = a.err;

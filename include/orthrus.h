@@ -587,7 +587,12 @@ orthrus_status_t orthrus_ce_lm_head(const void *h, const void *w, int32_t dtype,
  * overwritten.  An ignored row, and a row whose dloss is 0, has a zero dh
  * and takes no part in dw, whatever its h and lse hold.  On the bf16 path dz
  * is rounded to bf16 before its two products (the operand type of the tensor
- * cores). */
+ * cores), and the logits are the tensor cores' sums, which truncate by up to
+ * about 1e-5 of a logit; the target's logit is taken again, so that dz of a
+ * likely target keeps its digits.  There it is as good as z - lse: a row whose
+ * 1 - p is 1e-4 sees the rounding of an fp32 lse near 16 (up to 1e-6) as 1 %.
+ * An lse from the truncated logits themselves (an ignored row's, or
+ * orthrus_kl_lm_head's) would be off by the truncation. */
 orthrus_status_t orthrus_ce_lm_head_grad_workspace(int32_t rows, int32_t hidden, int32_t vocab, int32_t dtype,
                                                    int32_t weight_grad, size_t *bytes);
 orthrus_status_t orthrus_ce_lm_head_grad(const void *h, const void *w, int32_t dtype, const int32_t *targets,
