@@ -151,8 +151,8 @@ __device__ void simt_tile(const Operand<TA> &A, const Operand<TB> &B, int m0, in
 // exp(-inf) (a NaN among them still makes the sum a NaN).
 __device__ __forceinline__ float exp_shift(float m) { return m == -INFINITY ? 0.f : m; }
 
-// Forward: per (64-id tile, row) maximum and sum of exponentials, and the
-// logit of the row's target.
+// Forward: per (64-id tile, row) maximum and sum of exponentials of the ids but
+// the row's target, and the target's logit.
 template <class T>
 __global__ void __launch_bounds__(kStThreads) ce_tile_simt(const T *h, const T *w, const int32_t *targets, int N, int d,
                                                            int V, float2 *rec, float *zt)
@@ -172,35 +172,42 @@ __global__ void __launch_bounds__(kStThreads) ce_tile_simt(const T *h, const T *
         for (int j = 0; j < 4; ++j) sm.z[ty * 4 + i][tx * 4 + j] = acc[i][j];
     __syncthreads();
     const int r = threadIdx.x >> 2, q = threadIdx.x & 3, row = m0 + r, nv = min(kSt, V - n0);
+    const int t = row < N ? targets[row] : -1, tc = t < 0 ? -1 : t - n0;   // the target's column, if below nv
     float m = -INFINITY, s = 0.f;
-    for (int c = q; c < nv; c += 4) m = fmaxf(m, sm.z[r][c]);
+    for (int c = q; c < nv; c += 4)
+        if (c != tc) m = fmaxf(m, sm.z[r][c]);
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const float sh = exp_shift(m);
-    for (int c = q; c < nv; c += 4) s += expf(sm.z[r][c] - sh);
+    for (int c = q; c < nv; c += 4)
+        if (c != tc) s += expf(sm.z[r][c] - sh);
     s += __shfl_xor_sync(0xffffffffu, s, 1);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
     if (q == 0 && row < N) {
         rec[(size_t)blockIdx.x * N + row] = make_float2(m, s);
-        const int t = targets[row];
-        if (t >= n0 && t < n0 + nv) zt[row] = sm.z[r][t - n0];
+        if (tc >= 0 && tc < nv) zt[row] = sm.z[r][tc];
     }
 }
 
 // lse and loss from the tiles' records: rx rows x 1024 / rx strands of tiles
 // per block (few rows: many strands, or one row's records would be read one
 // after the other).
+// The target joins last: with a = log sum_{v != t} exp(z_v) - z_t the loss is
+// log(1 + exp a), which keeps its digits where the target is likely (lse - z_t
+// would be off by the rounding of lse, 1e-6 at 16, and by that of a sum of tiles
+// near 1: at p = 0.9999 5 % of the loss).
 // EXACT (tensor-core path): the tensor cores' accumulator truncates, which
 // moves a logit by up to ~1e-5 of itself.  Over the vocabulary that averages
-// out, but the target's logit enters the loss alone, so it is taken again as
-// an fp32 dot product and replaces its first value in the sum as well.
+// out, but the target's logit enters the loss alone, so it is taken again, in
+// fp32 parts and a double sum.
 constexpr int kFinThreads = 1024;
 
 template <bool EXACT>
 __global__ void __launch_bounds__(kFinThreads) ce_finalize_kernel(const float2 *rec, const float *zt, LossArgs a,
                                                                   int n_tiles, int rx)
 {
-    __shared__ float sm[kFinThreads], ss[kFinThreads], sz[32];
+    __shared__ float sm[kFinThreads], ss[kFinThreads];
+    __shared__ double sz[32];
     pdl_trigger();
     pdl_wait();
     const int N = a.N, V = a.V, strands = kFinThreads / rx;
@@ -215,7 +222,7 @@ __global__ void __launch_bounds__(kFinThreads) ce_finalize_kernel(const float2 *
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
                 for (int i = lane; i < a.d / 8; i += 32) dot8(ph[i], pw[i], acc);
-                const float z = warp_sum((acc[0] + acc[1]) + (acc[2] + acc[3]));
+                const double z = warp_sum_f64((double)(acc[0] + acc[1]) + (double)(acc[2] + acc[3]));
                 if (lane == 0) sz[w] = z;
             }
         }
@@ -249,17 +256,20 @@ __global__ void __launch_bounds__(kFinThreads) ce_finalize_kernel(const float2 *
     if (y || row >= N) return;
     const int t = a.targets[row];
     const bool live = t >= 0 && t < V;
-    float z = live ? zt[row] : 0.f;
-    if (EXACT && live) {
-        s += expf(sz[x] - exp_shift(m)) - expf(z - exp_shift(m));
-        z = sz[x];
-    }
-    const float L = m + logf(s);
-    a.lse[row] = L;
     if (t >= V && a.err) raise_err(a.err, ORTHRUS_DEVERR_TOKEN);
-    if (!live) { a.loss[row] = 0.f; return; }
+    const float rest = m + logf(s);   // the ids but the target
+    if (!live) {
+        a.lse[row] = rest;
+        a.loss[row] = 0.f;
+        return;
+    }
+    const double z = EXACT ? sz[x] : (double)zt[row];
+    const float x_t = (float)z, d = (float)((double)m - z) + logf(s);
+    const float e = log1pf(expf(-fabsf(d)));
+    const float L = x_t == -INFINITY ? rest : d > 0.f ? rest + e : (float)(z + (double)e);
+    a.lse[row] = L;
     if (!isfinite(L) && a.err) raise_err(a.err, ORTHRUS_DEVERR_NONFINITE);
-    a.loss[row] = L - z;
+    a.loss[row] = !isfinite(L) ? L - x_t : d > 0.f ? d + e : e;
 }
 
 cudaError_t launch_ce_finalize(const float2 *rec, const float *zt, const LossArgs &a, int n_tiles, int exact,

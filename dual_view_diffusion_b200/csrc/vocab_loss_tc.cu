@@ -8,7 +8,8 @@
 // 128-row tiles, which is what held those back).  What differs between the
 // products is the operands' order in memory and the epilogue:
 //
-//   LSE   z = h W^T          epilogue: (max, sum exp) per (row, tile), target logit
+//   LSE   z = h W^T          epilogue: (max, sum exp) per (row, tile) of the ids
+//                            but the target
 //   DZ    z = h W^T          epilogue: dz = g exp(z - lse), the target's from
 //                            vl_target_kernel, bf16
 //   DZKL  z of interleaved (AR, diffusion) rows: dz = g (p_diff - p_AR), bf16
@@ -83,7 +84,6 @@ struct VlJob {
     const float *lse, *lse2, *g;
     const float *et;     // DZ, DZ_T: exp(z - lse) - 1 of the rows' targets
     float2 *rec;         // LSE: [nt][M]; LSE_T: [groups of 32 ids][N]
-    float *zt;           // LSE: the rows' target logits
     bf16 *dz;            // DZ_T: [rows][pitch]
     int v0, V, pitch;    // DZ: the piece's first id, the vocabulary, dz's row length
     float *part;         // DH: [splits][M][N] fp32
@@ -264,7 +264,7 @@ __device__ __forceinline__ bool vl_epi_lse(const VlJob &jb, const VlTile &x, int
 {
     const int nv = min(jb.bn, jb.N - x.n0);           // ids of this tile below the vocabulary
     const int id = row < jb.M ? jb.targets[row] : -1, t = id < 0 ? -1 : id - x.n0;
-    float m = -INFINITY, s = 0.f, z_t = 0.f;
+    float m = -INFINITY, s = 0.f;
     for (int c = 32 * half; c < nv; c += 64) {
         float r[32];
         vl_tmem_ld32(taddr + c, r);
@@ -275,7 +275,7 @@ __device__ __forceinline__ bool vl_epi_lse(const VlJob &jb, const VlTile &x, int
         if (t >= c && t < c + 32)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                if (t == c + i) z_t = r[i];
+                if (t == c + i) r[i] = -INFINITY;   // (ce_finalize_kernel adds it)
         float cm = r[0];
 #pragma unroll
         for (int i = 1; i < 32; ++i) cm = fmaxf(cm, r[i]);
@@ -296,7 +296,6 @@ __device__ __forceinline__ bool vl_epi_lse(const VlJob &jb, const VlTile &x, int
     } else if (!__all_sync(0xffffffffu, vl_wait(bar, parity, abort))) {
         return false;
     }
-    if (row < jb.M && t >= 0 && t < nv && (t >> 5 & 1) == half) jb.zt[row] = z_t;
     if (row < jb.M && !half) {
         const float2 o = *other;
         const float mn = fmaxf(m, o.x), k = (mn == -INFINITY ? 0.f : mn) * kLog2e;
@@ -486,9 +485,8 @@ __device__ __forceinline__ void vl_epi_lse_t(const VlJob &jb, int v, uint32_t ta
         const int tgt = c + lane < jb.N ? jb.targets[c + lane] : -1;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-            if (v >= jb.M) r[j] = -INFINITY;
             const int t = __shfl_sync(0xffffffffu, tgt, j);
-            if (t == v && v < jb.M) jb.zt[c + j] = r[j];
+            if (v >= jb.M || t == v) r[j] = -INFINITY;   // (the target: ce_finalize_kernel adds it)
             const float mj = warp_max_f32(r[j]), k = (mj == -INFINITY ? 0.f : mj) * kLog2e;
             r[j] = vl_exp2(fmaf(r[j], kLog2e, -k));
             if (lane == j) m = mj;
@@ -829,14 +827,12 @@ size_t loss_fwd_workspace_tc(int N, int d, int V)
 {
     WsPlan w;
     w.take((size_t)(vl_narrow(N) ? (V + 31) / 32 : (V + kVlNMax - 1) / kVlNMax) * N * sizeof(float2));
-    w.take((size_t)N * 4);
     return w.total;
 }
 
 cudaError_t loss_fwd_tc(const LossArgs &a, cudaStream_t s)
 {
     float2 *rec = (float2 *)a.ws;
-    float *zt = (float *)(a.ws + loss_fwd_workspace_tc(a.N, a.d, a.V) - (((size_t)a.N * 4 + 255) & ~(size_t)255));
     VlParams p;
     memset(&p, 0, sizeof(p));
     VlJob &j = p.job;
@@ -846,14 +842,14 @@ cudaError_t loss_fwd_tc(const LossArgs &a, cudaStream_t s)
     j.kind = narrow ? VL_LSE_T : VL_LSE; j.M = rows; j.N = cols; j.chunks = (a.d + kVlK - 1) / kVlK; j.splits = 1;
     j.bn = narrow ? vl_narrow_bn(a.N) : kVlNMax;
     j.mt = (rows + kVlM - 1) / kVlM; j.nt = (cols + j.bn - 1) / j.bn;
-    j.targets = a.targets; j.rec = rec; j.zt = zt;
+    j.targets = a.targets; j.rec = rec;
     if (!make_tmap_box(&j.a, narrow ? a.w : a.h, rows, a.d, 64, 128) ||
         !make_tmap_box(&j.b, narrow ? a.h : a.w, cols, a.d, 64, j.bn / 2))
         return cudaErrorInvalidValue;
     p.err = a.err;
     cudaError_t e = vl_launch(p, s);
     if (e != cudaSuccess) return e;
-    return launch_ce_finalize(rec, zt, a, narrow ? (a.V + 31) / 32 : j.nt, 1, s);
+    return launch_ce_finalize(rec, nullptr, a, narrow ? (a.V + 31) / 32 : j.nt, 1, s);
 }
 
 struct VlPlan {

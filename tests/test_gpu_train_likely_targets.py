@@ -94,3 +94,98 @@ def test_target_logit_of_one_sign(n):
     tol = 2 * half(BF) + 4 * U * zt / one_minus
     e = rel_rows(dh, want)
     assert bool((e <= tol).all()), float((e / tol).max())
+
+
+@pytest.mark.parametrize("dt,n,d,V", SHAPES)
+def test_loss_of_likely_targets(dt, n, d, V):
+    """The loss of a likely target is small: its own digits count, not lse's."""
+    h, w, t, up = likely_rows(n, d, V, dt)
+    H, W, ti = h.to(F64), w.to(F64), t.long()[:, None]
+    z = H @ W.T
+    zt = z.gather(1, ti)[:, 0]
+    rest = torch.logsumexp(z.scatter(1, ti, -math.inf), 1)
+    want = torch.nn.functional.softplus(rest - zt)
+    assert float(want.min()) < 2e-4 and float(want.max()) > 0.05
+    loss, lse = pkg.orthrus_ce_lm_head(h, w, t)
+    # |d loss / loss| is at most the error of rest - z_t: of the other logits (bf16:
+    # d / 16 truncated additions; else fp32 sums in groups of 128), of z_t, of the
+    # exponentials' sum (2^-18) and of the logarithm
+    mag = (H.abs() @ W.abs().T).amax(1)
+    tc = dt == BF and d % 8 == 0
+    rerr = (2 * U * d / 16 if tc else 8 * U) * mag
+    zerr = 4 * U * zt.abs() if tc else 8 * U * (H.abs() * W[t.long()].abs()).sum(1)
+    tol = rerr + zerr + 2.0 ** -18 + 4 * U * (rest.abs() + zt.abs())
+    e = (loss.to(F64) - want).abs() / want
+    assert bool((e <= tol).all()), (float((e / tol).max()), float(e.max()))
+    L = torch.logsumexp(z, 1)
+    tol = U * L.abs() + zerr + tol * want
+    e = (lse.to(F64) - L).abs()
+    assert bool((e <= tol).all()), float((e / tol).max())
+    # what the gradient makes of it: 1 - p off by lse's half step and no more
+    dh, _ = pkg.orthrus_ce_lm_head_grad(h, w, t, lse, up, weight_grad=False)
+    p = torch.softmax(z, 1)
+    one_minus = -torch.expm1(zt - L)
+    dz = p.scatter(1, ti, -one_minus[:, None]) * up.to(F64)[:, None]
+    # (z_t's error enters through lse as well as in the gradient's own z - lse)
+    tol = (2 * half(dt) + 1e-4 if dt == BF else 1e-5 + 2 * d * U) + (U * L.abs() + 2 * zerr + 2.0 ** -23) / one_minus
+    e = rel_rows(dh, dz @ W)
+    assert bool((e <= tol).all()), float((e / tol).max())
+
+
+@pytest.mark.parametrize("n", [20, 300])
+def test_loss_of_one_sign(n):
+    """As test_target_logit_of_one_sign: all of the loss's error is z_t's, which
+    the tensor cores' truncated sum would put 1e-5 of z_t off."""
+    d, V, t0 = 4096, 3000, 17
+    g = torch.Generator(device=DEV)
+    g.manual_seed(52)
+    w = torch.zeros((V, d), dtype=BF, device=DEV)
+    w[t0] = (0.5 + torch.rand((d,), generator=g, device=DEV)).to(BF)
+    h = (0.5 + torch.rand((n, d), generator=g, device=DEV))
+    h = (h * torch.linspace(-4, 17, n, device=DEV)[:, None] / (h @ w[t0].float())[:, None]).to(BF)
+    t = torch.full((n,), t0, dtype=torch.int32, device=DEV)
+    zt = h.to(F64) @ w[t0].to(F64)
+    loss, lse = pkg.orthrus_ce_lm_head(h, w, t)
+    a = math.log(V - 1) - zt
+    want = torch.nn.functional.softplus(a)
+    e = (loss.to(F64) - want).abs() / want
+    # a in fp32 (two roundings of at most |z| + log V), log and exp two steps each
+    tol = U * (2 * zt.abs() + 4 * math.log(V) + 8)
+    assert bool((e <= tol).all()), float((e / tol).max())
+    L = zt + want
+    assert bool(((lse.to(F64) - L).abs() <= U * (L.abs() + 16)).all())
+
+
+@pytest.mark.parametrize("dt,d", [(BF, 64), (BF, 60), (F32, 64)])
+@pytest.mark.parametrize("n", [3, 270])
+def test_losses_at_the_ends(dt, d, n):
+    """One id; a target or all else at -inf; every id at -inf; a target at +inf."""
+    inf = math.inf
+    h = torch.zeros((n, d), dtype=dt, device=DEV)
+    h[:, 0] = 1
+    t = torch.zeros(n, dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    one = torch.zeros((1, d), dtype=dt, device=DEV)
+    one[0, 0] = 3
+    loss, lse = pkg.orthrus_ce_lm_head(h, one, t, err=err)
+    assert bool((loss == 0).all()) and bool((lse == 3).all()) and int(err) == 0
+    w = torch.zeros((70, d), dtype=dt, device=DEV)
+    w[0, 0] = -inf
+    loss, lse = pkg.orthrus_ce_lm_head(h, w, t, err=err)
+    assert bool((loss == inf).all()) and bool(((lse - math.log(69)).abs() < 1e-6).all()) and int(err) == 0
+    w[:, 0] = -inf
+    w[0, 0] = 2
+    loss, lse = pkg.orthrus_ce_lm_head(h, w, t, err=err)
+    assert bool((loss == 0).all()) and bool((lse == 2).all()) and int(err) == 0
+    w[0, 0] = -inf
+    loss, lse = pkg.orthrus_ce_lm_head(h, w, t, err=err)
+    assert bool((lse == -inf).all()) and bool(loss.isnan().all()) and int(err) == 4
+    err.zero_()
+    w[0, 0] = inf
+    loss, lse = pkg.orthrus_ce_lm_head(h, w, t, err=err)
+    assert bool((lse == inf).all()) and bool(loss.isnan().all()) and int(err) == 4
+    # an ignored row's lse is of the whole vocabulary
+    w[:, 0] = 0
+    w[0, 0] = 4
+    lse = pkg.orthrus_ce_lm_head(h, w, torch.full_like(t, -1))[1]
+    assert bool(((lse - math.log(math.exp(4) + 69)).abs() < 1e-5).all())
