@@ -827,7 +827,9 @@ cudaError_t launch_norm_rows(const NormArgs &a, cudaStream_t s)
 
 // Gradient.  With u = g dy, A = sum x^2, B = sum u x over a row and
 // r = (A/d + eps)^-1/2:
-//     dx = r u - r^3 (B/d) x,     dgain = sum over rows of dy x r.
+//     dx = r u - k x, k = r^2 (r B / d),     dgain = sum over rows of dy x r.
+// k's factors in that order: r^3 leaves fp32 where k does not (rows of 1e-14
+// with eps = 0, or of 1e15), r^2 only where the row's sum of squares does too.
 // One pass: a row's x and dy are read once into registers, both sums are
 // reduced together, dx is written, and dgain's columns stay in the thread's
 // registers over all rows the block takes; each block leaves its column sums
@@ -895,7 +897,7 @@ __global__ void __launch_bounds__(kNgThreads, VEC * J == 8 ? 2 : 1)
         }
         // (two buffers: a block reads one while the next row writes the other)
         group_sum<G, 2>(s, red[flip]);
-        const float r = 1.0f / sqrtf(s[0] / (float)d + eps), k = r * r * r * (s[1] / (float)d);
+        const float r = 1.0f / sqrtf(s[0] / (float)d + eps), k = (r * r) * (r * (s[1] / (float)d));
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const int c = t + j * G;
@@ -947,7 +949,7 @@ __global__ void __launch_bounds__(kNgThreads) norm_grad_long_kernel(const TX *x,
         s[1] = fmaf(to_f<T>(yr[c]) * to_f<T>(gain[c]), xv, s[1]);
     }
     group_sum<kNgThreads, 2>(s, red);
-    const float r = 1.0f / sqrtf(s[0] / (float)d + eps), k = r * r * r * (s[1] / (float)d);
+    const float r = 1.0f / sqrtf(s[0] / (float)d + eps), k = (r * r) * (r * (s[1] / (float)d));
     if (threadIdx.x == 0) rstd[row] = r;
     for (int c = threadIdx.x; c < d; c += kNgThreads) {
         const float xv = to_f<TX>(xr[c]);

@@ -555,7 +555,9 @@ orthrus_status_t orthrus_embed_grad(const void *dout, int32_t dout_dtype, const 
 
 /* y = x * gain / sqrt(mean(x^2) + eps) per row: x [rows][hidden] (x_dtype: fp32,
  * the residual stream's, or dtype), gain [hidden] and y [rows][hidden] (dtype).
- * x in bf16 with gain and y in fp32 returns ORTHRUS_ERR_UNSUPPORTED. */
+ * x in bf16 with gain and y in fp32 returns ORTHRUS_ERR_UNSUPPORTED.  A row's
+ * sum of squares is fp32: rows of elements between about 1e-18 and 1e18 in
+ * magnitude are taken at any eps >= 0, smaller ones where eps is larger. */
 orthrus_status_t orthrus_rmsnorm(const void *x, int32_t x_dtype, const void *gain, int32_t dtype, int32_t rows,
                                  int32_t hidden, float eps, void *y, void *stream);
 
