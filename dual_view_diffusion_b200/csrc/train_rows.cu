@@ -213,6 +213,7 @@ cudaError_t launch_embed_rows(const EmbedRowsArgs &a, cudaStream_t s)
 // order give the same bits on every call (no floating-point atomics).
 // Ids outside [0, vocab) sort behind every token and are left out.
 constexpr int kRunThreads = 128;
+constexpr int kPieceMost = 4096;     // longest piece
 
 EmbedGradPlan plan_embed_grad(int rows, int vocab, int d)
 {
@@ -232,7 +233,7 @@ EmbedGradPlan plan_embed_grad(int rows, int vocab, int d)
     // about 1024 blocks, and partials per column, are the most
     const int slabs = (d + 8 * kRunThreads - 1) / (8 * kRunThreads);
     p.piece = 8;
-    while (p.piece < 4096 && (long)(rows / p.piece) * slabs > 1024) p.piece *= 2;
+    while (p.piece < kPieceMost && (long)(rows / p.piece) * slabs > 1024) p.piece *= 2;
     p.pieces = (rows + p.piece - 1) / p.piece;
     p.o_part = w.take((size_t)p.pieces * 2 * d * 4);
     p.total = w.total;
@@ -636,8 +637,10 @@ static cudaError_t run_sums(const EmbedGradArgs &a, const EmbedGradPlan &p, cons
     const int units = (a.vocab - zero_from + unit - 1) / unit, per = kRunThreads / 32;
     const int fill_blocks = (units + per - 1) / per;
     auto sum = [&](auto kernel) {
-        if (p.piece > 1024) {   // its tokens beside the rows in flight: more than the 48 KiB of a plain launch
-            const cudaError_t ea = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, p.piece * 8);
+        // a long piece's tokens beside the rows in flight: more than the 48 KiB of a plain launch (the limit is the
+        // process's, so it is set to the most that any call needs: another thread's call may lie between the two)
+        if (p.piece > 1024) {
+            const cudaError_t ea = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPieceMost * 8);
             if (ea != cudaSuccess) return ea;
         }
         return launch_k(kernel, run_blocks + fill_blocks, kRunThreads, (size_t)p.piece * 8, s, (const T *)a.dout, tok, idx,
