@@ -96,6 +96,7 @@ _SIGS = {
     "orthrus_commit_adaptive": [_P, C.POINTER(KV), _I, _I, _P, _P, _P, _P, _P, _P],
     "orthrus_check_error": [_P, _P, C.POINTER(C.c_uint32)],
     "orthrus_set_probe": [_P, _I, _I, _I, C.POINTER(_P), C.POINTER(_P), _I],
+    "orthrus_train_check_error": [_P, C.POINTER(C.c_uint32)],
     "orthrus_embed_rows": [_P, _I, _I, _I, _P, _I, C.c_float, _P, _I, _P, _P],
     "orthrus_embed_grad_workspace": [_I, _I, _I, C.POINTER(C.c_size_t)],
     "orthrus_embed_grad": [_P, _I, _P, _I, _I, _I, C.c_float, _I, _P, _I, _P, C.c_size_t, _P, _P],
@@ -178,7 +179,9 @@ def _need(x, dtype, name):
 # -------------------------------------------- training-side operators
 # Context-free mirrors: outputs and workspaces come from torch's allocator on
 # the tensors' device and that device's current stream.  `err` is an optional
-# int32 device tensor of one element that collects the ORTHRUS_DEVERR_* bits.
+# int32 device tensor of one element that collects the ORTHRUS_DEVERR_* bits;
+# without it they collect in the library's word of that device, for
+# orthrus_train_check_error.
 _torch = None   # the module, imported by the first call
 _DT = None      # torch dtype -> orthrus_dtype_t
 
@@ -251,6 +254,24 @@ def _err_ptr(err, device):
         return None
     _need_rows("err", err, (_torch.int32,), (1,), device)
     return err.data_ptr()
+
+
+def orthrus_train_check_error(device=None):
+    """The ORTHRUS_DEVERR_* bits that the calls without `err` have raised on
+    `device` (default: the current one) so far, 0 for none; read and cleared.
+    Waits for that device's current stream."""
+    _dtypes()
+    device = _torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError(f"device: expected a CUDA device, got {device}")
+    if device.index is None:
+        device = _torch.device("cuda", _torch.cuda.current_device())
+    bits = C.c_uint32()
+    with _OnDevice(device) as stream:
+        status = lib().orthrus_train_check_error(stream, C.byref(bits))
+    if not bits.value:
+        _check("orthrus_train_check_error", status)
+    return bits.value
 
 
 def orthrus_embed_rows(table, ids, scale=1.0, out_dtype=None, err=None):

@@ -15,6 +15,11 @@ using namespace orthrus;
 
 namespace {
 
+// the check bits of the calls that name no word of their own, one word per device
+__device__ unsigned own_err_word;
+
+__global__ void clear_bits_kernel(unsigned *word, unsigned bits) { atomicAnd(word, ~bits); }
+
 constexpr int32_t kMostRows = 4000000, kMostHidden = 65536;
 
 bool dtype_ok(int32_t t) { return t == ORTHRUS_BF16 || t == ORTHRUS_FP32; }
@@ -40,6 +45,16 @@ orthrus_status_t ws_ok(const void *ws, size_t have, size_t need)
     return have < need ? ORTHRUS_ERR_CAPACITY : ORTHRUS_OK;
 }
 
+// where a call of `rows` rows raises its bits
+orthrus_status_t err_word(uint32_t *&dev_err, int32_t rows)
+{
+    if (dev_err || rows == 0) return ORTHRUS_OK;
+    void *p = nullptr;
+    CK(cudaGetSymbolAddress(&p, own_err_word));
+    dev_err = (uint32_t *)p;
+    return ORTHRUS_OK;
+}
+
 }  // namespace
 
 #define OK(x)                                          \
@@ -59,6 +74,7 @@ orthrus_status_t orthrus_embed_rows(const void *table, int32_t dtype, int32_t vo
         !ptr_ok(ids, ORTHRUS_FP32, rows > 0) || !ptr_ok(out, out_dtype, rows > 0) || !ptr_ok(dev_err, ORTHRUS_FP32, false))
         return ORTHRUS_ERR_INVALID_ARG;
     if (rows == 0) return ORTHRUS_OK;
+    OK(err_word(dev_err, rows));
     CK(launch_embed_rows(EmbedRowsArgs{table, ids, out, dtype, out_dtype, rows, hidden, vocab, scale, dev_err},
                          (cudaStream_t)stream));
     return ORTHRUS_OK;
@@ -85,6 +101,7 @@ orthrus_status_t orthrus_embed_grad(const void *dout, int32_t dout_dtype, const 
     size_t need;
     OK(orthrus_embed_grad_workspace(rows, hidden, vocab, &need));
     OK(ws_ok(workspace, ws_bytes, need));
+    OK(err_word(dev_err, rows));
     CK(launch_embed_grad(EmbedGradArgs{dout, ids, dtable, dout_dtype, dtable_dtype, rows, hidden, vocab, accumulate, scale,
                                        (char *)workspace, dev_err},
                          (cudaStream_t)stream));
@@ -157,6 +174,7 @@ orthrus_status_t orthrus_ce_lm_head(const void *h, const void *w, int32_t dtype,
     size_t need;
     OK(orthrus_ce_lm_head_workspace(rows, hidden, vocab, dtype, &need));
     OK(ws_ok(workspace, ws_bytes, need));
+    OK(err_word(dev_err, rows));
     LossArgs a{};
     a.h = h; a.w = w; a.targets = targets; a.loss = loss; a.lse = lse; a.dtype = dtype; a.N = rows; a.d = hidden;
     a.V = vocab; a.ws = (char *)workspace; a.err = dev_err;
@@ -187,6 +205,7 @@ orthrus_status_t orthrus_ce_lm_head_grad(const void *h, const void *w, int32_t d
     size_t need;
     OK(orthrus_ce_lm_head_grad_workspace(rows, hidden, vocab, dtype, dw != nullptr, &need));
     OK(ws_ok(workspace, ws_bytes, need));
+    OK(err_word(dev_err, rows));
     LossArgs a{};
     a.h = h; a.w = w; a.targets = targets; a.lse_in = lse; a.g = dloss; a.dh = dh; a.dw = dw; a.dtype = dtype;
     a.N = rows; a.d = hidden; a.V = vocab; a.ws = (char *)workspace; a.err = dev_err;
@@ -218,11 +237,31 @@ orthrus_status_t orthrus_kl_lm_head_grad(const void *h_ar, const void *h_diff, c
     size_t need;
     OK(orthrus_kl_lm_head_grad_workspace(rows, hidden, vocab, dtype, &need));
     OK(ws_ok(workspace, ws_bytes, need));
+    OK(err_word(dev_err, rows));
     LossArgs a{};
     a.h = h_ar; a.h2 = h_diff; a.w = w; a.lse_in = lse_ar; a.lse2_in = lse_diff; a.g = dkl; a.dh = dh_diff;
     a.dtype = dtype; a.N = rows; a.d = hidden; a.V = vocab; a.kl = 1; a.ws = (char *)workspace; a.err = dev_err;
     CK(launch_loss_grad(a, (cudaStream_t)stream));
     return ORTHRUS_OK;
+}
+
+orthrus_status_t orthrus_train_check_error(void *stream, uint32_t *bits)
+{
+    if (!bits) return ORTHRUS_ERR_INVALID_ARG;
+    cudaStream_t s = (cudaStream_t)stream;
+    void *p = nullptr;
+    unsigned h = 0;
+    CK(cudaGetSymbolAddress(&p, own_err_word));
+    CK(cudaMemcpyAsync(&h, p, 4, cudaMemcpyDeviceToHost, s));
+    CK(cudaStreamSynchronize(s));
+    if (h) {   // (only what is reported: another stream may raise more meanwhile)
+        clear_bits_kernel<<<1, 1, 0, s>>>((unsigned *)p, h);
+        CK(cudaGetLastError());
+        CK(cudaStreamSynchronize(s));
+    }
+    *bits = h;
+    if (h & ORTHRUS_DEVERR_NONFINITE) return ORTHRUS_ERR_NONFINITE;
+    return h ? ORTHRUS_ERR_DEVICE_CHECK : ORTHRUS_OK;
 }
 
 }  // extern "C"

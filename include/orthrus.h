@@ -525,12 +525,20 @@ orthrus_status_t orthrus_tree_commit(orthrus_ctx_t *ctx, const orthrus_kv_t *kv,
  *   - everything is enqueued on `stream`, on the current device; nothing is
  *     allocated or synchronised.  Calls may be captured; two calls may run at
  *     the same time on one GPU when their workspaces and outputs differ.
- *   - dev_err: device uint32 of the caller or NULL.  ORTHRUS_DEVERR_* bits of
- *     problems that only the device can see are ORed into it; it is never
- *     cleared here.
+ *   - dev_err: device uint32 of the caller, or NULL for a word of the library's
+ *     own, one per device, which orthrus_train_check_error reads and clears.
+ *     ORTHRUS_DEVERR_* bits of problems that only the device can see are ORed
+ *     into it; the calls themselves never clear it.  After
+ *     ORTHRUS_DEVERR_TIMEOUT the call's outputs are not to be used.
  *   - Sums are held in fp32 and taken in an order that the shapes alone fix,
  *     so a call repeated on the same inputs gives the same bits.
  */
+
+/* The bits that calls without a dev_err of their own have raised on the current
+ * device, in *bits; they are cleared.  Synchronises `stream` (work on other
+ * streams may still be running), which must not be capturing.  Returns
+ * ORTHRUS_ERR_NONFINITE or ORTHRUS_ERR_DEVICE_CHECK when bits are set. */
+orthrus_status_t orthrus_train_check_error(void *stream, uint32_t *bits);
 
 /* out[r] = scale * table[ids[r]].  table [vocab][hidden] (dtype), ids int32
  * [rows], out [rows][hidden] (out_dtype; the residual stream of the decode path
