@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kStThreads) dz_tile_simt(LossArgs a, int v0, i
             if (v >= vend) continue;
             float x;
             if (KL) x = expf(z2[i][j] - lse2) - expf(z[i][j] - lse);
-            else x = v == t ? expm1f(z[i][j] - lse) : expf(z[i][j] - lse);   // (a likely target's 1 - p keeps its digits)
+            else x = expf(z[i][j] - lse) - (v == t ? 1.f : 0.f);   // (z's and lse's own half steps are larger than 1's)
             dz[(size_t)row * Vp + (v - v0)] = g == 0.f ? 0.f : g * x;
         }
     }
