@@ -632,13 +632,21 @@ class Engine:
 
     # training-side operators over the engine's own weights (their device
     # checks collect in train_err)
+    def _ids(self, x):
+        """Token ids as int32; an id past its range stays out of every vocabulary
+        (cut to 32 bits, 2^32 + 5 would be id 5)."""
+        t = self.torch
+        if isinstance(x, t.Tensor) and x.dtype == t.int64:
+            x = x.clamp(-1, 2 ** 31 - 1)
+        return self._i32(x)
+
     def embed_rows(self, ids, scale=1.0):
-        """scale * embed[ids]: the fp32 residual rows of int32 ids [rows]."""
-        return orthrus_embed_rows(self.embed, self._i32(ids), scale, err=self.train_err)
+        """scale * embed[ids]: the fp32 residual rows of ids [rows]."""
+        return orthrus_embed_rows(self.embed, self._ids(ids), scale, err=self.train_err)
 
     def embed_grad(self, dout, ids, scale=1.0, out=None, accumulate=False):
         """Gradient of embed_rows in the embedding table."""
-        return orthrus_embed_grad(dout, self._i32(ids), self.shape.vocab, scale, out=out, accumulate=accumulate,
+        return orthrus_embed_grad(dout, self._ids(ids), self.shape.vocab, scale, out=out, accumulate=accumulate,
                                   err=self.train_err)
 
     def final_norm_rows(self, x):
@@ -653,12 +661,12 @@ class Engine:
     def ce_lm_head(self, h, targets):
         """Cross entropy of final-normed rows h through the LM head: (loss,
         lse), fp32 [rows]."""
-        return orthrus_ce_lm_head(h, self.lm_head, self._i32(targets), err=self.train_err)
+        return orthrus_ce_lm_head(h, self.lm_head, self._ids(targets), err=self.train_err)
 
     def ce_lm_head_grad(self, h, targets, lse, dloss, weight_grad=True):
         """(dh, dw) of ce_lm_head; weight_grad False leaves dw out (a frozen
         head)."""
-        return orthrus_ce_lm_head_grad(h, self.lm_head, self._i32(targets), lse, dloss, weight_grad,
+        return orthrus_ce_lm_head_grad(h, self.lm_head, self._ids(targets), lse, dloss, weight_grad,
                                        err=self.train_err)
 
     def kl_lm_head_grad(self, h_ar, h_diff, lse_ar, lse_diff, dkl):
