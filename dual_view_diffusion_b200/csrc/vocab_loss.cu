@@ -1,7 +1,7 @@
 // Losses through the shared LM head without keeping the logits: the cross
 // entropy of one token id per row with its gradients, and the gradient of
 // the forward KL(p_AR || p_diff) (paper notes §3.3).  With z = W h:
-//     CE   lse = log sum_v exp z_v,  loss = lse - z_t,
+//     CE   lse = log sum_v exp z_v,  loss = lse - z_t = log(1 + sum_{v != t} exp(z_v - z_t)),
 //          dz_v = g (exp(z_v - lse) - [v = t])
 //     KL   dz_v = g (softmax(W h_diff)_v - softmax(W h_AR)_v)
 //     dh = dz W,   dW = dz^T h.
@@ -419,7 +419,8 @@ static SimtPlan plan_simt(int N, int d, int V, int want_dw)
 {
     SimtPlan p{};
     WsPlan w;
-    // a piece's dz stays within 64 MiB
+    // a piece's dz stays within 64 MiB (past 262144 rows, 256 bytes per row: a
+    // piece has 64 ids at least)
     const size_t cap = std::max<size_t>(kSt, ((size_t)64 << 20) / (4 * (size_t)std::max(N, 1)) / kSt * kSt);
     p.piece = (int)std::min<size_t>(cap, ((size_t)V + kSt - 1) / kSt * kSt);
     // dh has few tiles at small N and d: its k axis (the piece) is cut until

@@ -33,12 +33,12 @@
 // ORTHRUS_DEVERR_TIMEOUT, stops issuing, lets its copies land and still frees
 // its TMEM.
 //
-// Measured: 4096 rows of 4096 over 151936 ids, forward 3.4 to 3.6 ms (1.4 to 1.5
+// Measured: 4096 rows of 4096 over 151936 ids, forward 3.4 to 3.7 ms (1.4 to 1.5
 // PFLOP/s, the sustained rate of a library product), both gradients 11.7 to 12.1 ms
 // (three products, 1.3 PFLOP/s; tensor pipe 80 to 87 % active, the rest the
-// ramps of a launch per product and piece, and L2 waits).  Few rows: one row of 2048, 113 us
-// of 97 for W's 622 MB; the gradients read W twice (31 rows: 207 us, of 193 for
-// that).  A narrow product is close to its own bound there too: each MMA takes
+// ramps of a launch per product and piece, and L2 waits).  Few rows: forward of one row of 2048, 113 us
+// of 97 for W's 622 MB; the gradients read W twice (31 rows: 204 us frozen head,
+// 206 to 210 KL, of 193 for that).  A narrow product is close to its own bound there too: each MMA takes
 // as long as a 256-column one, which passes W at 52 GB/s per SM.
 #include <cuda.h>
 #include <string.h>
@@ -774,7 +774,7 @@ static size_t up(size_t x, size_t m) { return (x + m - 1) / m * m; }
 // Up to kVlNMax rows ride as columns beside W's rows: a stage is then mostly
 // weights (measured at one row of 2048, vocabulary 151936: the 256-row tile of
 // h kept 48 KB of W in flight per SM and ran at 285 us, this one at 113; at 256
-// rows of 4096 this one takes 344 us, the 256-row tile at 257 rows 446).
+// rows of 4096 this one takes 398 us, the 256-row tile at 257 rows 548).
 static bool vl_narrow(int rows) { return rows <= kVlNMax; }
 static int vl_narrow_bn(int rows) { return (rows + 31) / 32 * 32; }
 
@@ -861,8 +861,8 @@ static VlPlan vl_plan(int N, int d, int V, int want_dw, int kl)
 {
     VlPlan p{};
     WsPlan w;
-    // a piece's dz stays within 256 MiB, bounded whatever the vocabulary, and
-    // large enough that a piece's products fill many rounds of the pairs and dh
+    // a piece's dz stays within 256 MiB (past 524288 rows, 512 bytes per row: a
+    // piece has 256 ids at least), whatever the vocabulary, and is large enough that a piece's products fill many rounds of the pairs and dh
     // is added up few times (both gradients, 4096 x 4096 x 151936: 13.3 ms at 64
     // MiB, 12.8 at 128, 12.4 at 256, 12.3 at 512)
     const size_t cap = std::max<size_t>(256, ((size_t)256 << 20) / (2 * (size_t)N) / 256 * 256);

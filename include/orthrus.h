@@ -530,8 +530,11 @@ orthrus_status_t orthrus_tree_commit(orthrus_ctx_t *ctx, const orthrus_kv_t *kv,
  *     ORTHRUS_DEVERR_* bits of problems that only the device can see are ORed
  *     into it; the calls themselves never clear it.  After
  *     ORTHRUS_DEVERR_TIMEOUT the call's outputs are not to be used.
- *   - Sums are held in fp32 and taken in an order that the shapes alone fix,
- *     so a call repeated on the same inputs gives the same bits.
+ *   - Sums are held in fp32 and taken in an order that the shapes, the types and
+ *     the buffers' alignment fix, so a call repeated on the same buffers gives
+ *     the same bits.  The tensor cores' sums truncate (of 4096 products, about
+ *     1e-5 of the sum).
+ *   - A logit beyond about 2e38 in magnitude may count as infinite.
  */
 
 /* The bits that calls without a dev_err of their own have raised on the current
@@ -578,7 +581,9 @@ orthrus_status_t orthrus_rmsnorm_grad(const void *x, int32_t x_dtype, const void
 
 /* Cross entropy through the LM head: per row, with z = w h,
  *     lse = log sum_v exp(z_v),   loss = lse - z[target],
- * over the whole vocabulary; the logits never reach memory.  h [rows][hidden]
+ * over the whole vocabulary; the logits never reach memory.  The target's
+ * logit joins the sum last, so that the loss of a likely target keeps its
+ * digits where lse - z[target] would not.  h [rows][hidden]
  * and w [vocab][hidden] (dtype), targets int32 [rows], loss and lse fp32
  * [rows].  A negative target is an ignored row (loss 0).  A target >= vocab
  * is ignored as well and raises ORTHRUS_DEVERR_TOKEN; a non-finite lse of a
@@ -615,8 +620,11 @@ orthrus_status_t orthrus_ce_lm_head_grad(const void *h, const void *w, int32_t d
  * upstream gradient dkl (fp32 [rows]):
  *     dz = dkl * (softmax(w h_diff) - softmax(w h_ar)),  dh_diff = dz w.
  * h_ar, h_diff, dh_diff [rows][hidden] and w [vocab][hidden] (dtype), lse_ar
- * and lse_diff fp32 [rows].  A row whose dkl is 0 has a zero dh_diff,
- * whatever its hidden rows hold.  Rounding of dz as above. */
+ * and lse_diff fp32 [rows], orthrus_kl_lm_head's or exact ones, both of one
+ * kind.  A row whose dkl is 0 has a zero dh_diff, whatever its hidden rows
+ * hold.  Rounding of dz as above; of an id that both views are nearly sure of
+ * it is the difference of two probabilities near 1, each off by the rounding of
+ * its fp32 lse and logit. */
 orthrus_status_t orthrus_kl_lm_head_grad_workspace(int32_t rows, int32_t hidden, int32_t vocab, int32_t dtype,
                                                    size_t *bytes);
 orthrus_status_t orthrus_kl_lm_head_grad(const void *h_ar, const void *h_diff, const void *w, int32_t dtype,
