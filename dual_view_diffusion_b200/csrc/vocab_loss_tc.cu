@@ -862,9 +862,10 @@ static VlPlan vl_plan(int N, int d, int V, int want_dw, int kl)
     VlPlan p{};
     WsPlan w;
     // a piece's dz stays within 256 MiB (past 524288 rows, 512 bytes per row: a
-    // piece has 256 ids at least), whatever the vocabulary, and is large enough that a piece's products fill many rounds of the pairs and dh
-    // is added up few times (both gradients, 4096 x 4096 x 151936: 13.3 ms at 64
-    // MiB, 12.8 at 128, 12.4 at 256, 12.3 at 512)
+    // piece has 256 ids at least), whatever the vocabulary, and is large enough
+    // that a piece's products fill many rounds of the pairs and dh is added up few
+    // times (both gradients, 4096 x 4096 x 151936: 13.3 ms at 64 MiB, 12.8 at 128,
+    // 12.4 at 256, 12.3 at 512)
     const size_t cap = std::max<size_t>(256, ((size_t)256 << 20) / (2 * (size_t)N) / 256 * 256);
     p.piece = (int)std::min(cap, up(V, 256));
     p.zrows = kl ? 2 * N : N;
